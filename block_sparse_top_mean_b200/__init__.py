@@ -18,6 +18,11 @@ from ._lib import (  # noqa: F401
     OP_SPARSE_ATTN_MIN, OP_PREFILL_MIN, OP_DECODE_OFFLOAD, OP_SPARSE_ATTN_BWD,
     OP_SPARSE_ATTN_BWD_MIN,
     DEVERR_IDX_RANGE, DEVERR_TIMEOUT, MSA_F32, MSA_BF16,
+    MsaPagedCache, OP_QK_NORM_ROPE_BWD, OP_PAGED_APPEND, OP_PAGED_ATTN, DEVERR_PAGE_RANGE,
+)
+from .layer import (  # noqa: F401
+    paged_append, paged_attn_fwd, paged_workspace, qk_norm_rope, qk_norm_rope_bwd,
+    qk_norm_rope_workspace,
 )
 
 __all__ = [
@@ -28,7 +33,9 @@ __all__ = [
     "clear_device_error", "version", "exp2_poly_eval", "rope_docwise", "prefill_varlen_fwd",
     "decode_select_shard", "decode_merge_shards", "decode_combine_shards", "decode_fwd_offload",
     "sparse_attn_bwd",
-    "MsaError", "MsaParams",
+    "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_workspace", "paged_append",
+    "paged_attn_fwd", "paged_workspace",
+    "MsaError", "MsaParams", "MsaPagedCache",
 ]
 
 _DT = {torch.float32: MSA_F32, torch.bfloat16: MSA_BF16}

@@ -14,8 +14,9 @@ MSA_OK, MSA_ERR_INVALID_ARG, MSA_ERR_UNSUPPORTED, MSA_ERR_WORKSPACE, MSA_ERR_CUD
     MSA_ERR_DEVICE, MSA_ERR_TIMEOUT = range(7)
 MSA_F32, MSA_BF16 = 0, 1
 OP_TOPK_SELECT, OP_SPARSE_ATTN, OP_PREFILL, OP_DECODE, OP_SPARSE_ATTN_MIN, OP_PREFILL_MIN, \
-    OP_DECODE_OFFLOAD, OP_SPARSE_ATTN_BWD, OP_SPARSE_ATTN_BWD_MIN = range(9)
-DEVERR_IDX_RANGE, DEVERR_TIMEOUT = 0x1, 0x2
+    OP_DECODE_OFFLOAD, OP_SPARSE_ATTN_BWD, OP_SPARSE_ATTN_BWD_MIN, OP_QK_NORM_ROPE_BWD, \
+    OP_PAGED_APPEND, OP_PAGED_ATTN = range(12)
+DEVERR_IDX_RANGE, DEVERR_TIMEOUT, DEVERR_PAGE_RANGE = 0x1, 0x2, 0x4
 
 # Every symbol include/msa.h declares, with (restype, argtypes).
 SIGNATURES = {
@@ -68,6 +69,18 @@ SIGNATURES = {
                                          c_size_t, c_void_p]),
     "msa_rope_docwise": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_double,
                                    c_void_p]),
+    "msa_qk_norm_rope": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                   c_int64, c_void_p, c_void_p, c_double, c_float, c_void_p,
+                                   c_void_p, c_void_p]),
+    "msa_qk_norm_rope_bwd": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int32,
+                                       c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p,
+                                       c_double, c_float, c_void_p, c_void_p, c_void_p, c_void_p,
+                                       c_void_p, c_size_t, c_void_p]),
+    "msa_paged_append": (c_int32, [c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int64,
+                                   c_void_p, c_int64, c_void_p, c_void_p, c_double, c_float,
+                                   c_void_p, c_void_p, c_size_t, c_void_p]),
+    "msa_paged_attn_fwd": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                     c_void_p, c_void_p, c_size_t, c_void_p]),
     "msa_prefill_varlen_fwd": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p,
                                          c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                          c_size_t, c_void_p]),
@@ -79,6 +92,13 @@ class MsaParams(ctypes.Structure):
     _fields_ = [("batch", c_int64), ("seq", c_int64), ("hq", c_int64), ("hkv", c_int64),
                 ("d", c_int64), ("block", c_int64), ("topk", c_int64), ("scale", c_float),
                 ("dtype", c_int32)]
+
+
+class MsaPagedCache(ctypes.Structure):
+    """Mirror of msa_paged_cache (include/msa.h)."""
+    _fields_ = [("k_pages", c_void_p), ("v_pages", c_void_p), ("page_table", c_void_p),
+                ("kv_lens", c_void_p), ("cu_seqlens", c_void_p), ("n_pages", c_int64),
+                ("max_pages", c_int64)]
 
 
 class MsaError(RuntimeError):

@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include "common.cuh"
+#include "paged.cuh"
 
 using msa::Shape;
 
@@ -193,6 +194,7 @@ const char* msa_status_string(msa_status st) {
 }
 
 size_t msa_workspace_bytes(const msa_params* p, int32_t op, int64_t n_query) {
+  if (op >= MSA_OP_QK_NORM_ROPE_BWD) return msa::layer_ws_bytes(p, op);
   Shape s;
   const bool dec = op == MSA_OP_DECODE || op == MSA_OP_DECODE_OFFLOAD;
   if (check_params(p, dec, &s) != MSA_OK) return 0;

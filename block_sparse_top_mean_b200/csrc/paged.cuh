@@ -1,0 +1,242 @@
+// Paged key/value caches: the shapes, the schedule of the attention kernels over them, and
+// the partial results that their CTAs leave for paged_combine_kernel.
+//
+// Pools k_pages, v_pages [n_pages, hkv, page, d]; sequence s holds kv_lens[s] tokens, token p
+// in slot p % page of page table[s][p / page]; its last n_s = cu[s+1] - cu[s] tokens are the
+// new ones, packed tokens cu[s].. of q and o.  A new token at position pos sees keys p <= pos.
+//
+// Rows.  The G = hq / hkv query heads of a KV head share its keys, so a row tile is TT tokens
+// x G heads (row = token * G + head) against tiles of KT keys.  An item is (sequence, KV
+// head, row tile); its key tiles are those up to its last token's position (at least one, so
+// that rows that see nothing are still written).
+//
+// Schedule.  All key tiles of all items, in order, are one line of W tiles that the CTAs cut
+// into equal runs (a run may start and end inside an item), so the work is even whatever the
+// lengths are: one long sequence, or many of very different lengths.  Every CTA finds its run
+// itself from cu and kv_lens (a scan over the sequences), so the lengths may change between
+// replays of a captured graph.  An item that one CTA holds whole is finished there; of one
+// that is cut, each CTA leaves its running maximum, sum and unnormalised output (fp32), and
+// the CTA that holds the item's first tile a record of how many parts there are.  Parts are
+// joined in order: results do not depend on timing.
+#pragma once
+
+#include <math_constants.h>
+
+#include "common.cuh"
+
+namespace msa {
+
+struct HeadShape {
+  int64_t n_tok, hq, hkv, d;
+  int dtype;
+};
+
+struct PagedShape {
+  const int32_t* table;               // [n_seqs, max_pages]
+  const int32_t* kv_lens;             // [n_seqs]
+  const int32_t* cu;                  // [n_seqs + 1]
+  int64_t n_seqs, max_pages, n_pages, page;
+};
+
+// qk_norm_rope.cu.  part: [qk_norm_rope_bwd_ctas()][2][d] fp32.
+int64_t qk_norm_rope_bwd_ctas();
+cudaError_t launch_qk_norm_rope(const HeadShape& s, const int32_t* cu, int64_t n_docs,
+                                const void* q, int64_t qs, const void* k, int64_t ks,
+                                const void* wq, const void* wk, double base, float eps, void* qo,
+                                void* ko, cudaStream_t st);
+cudaError_t launch_qk_norm_rope_bwd(const HeadShape& s, const int32_t* cu, int64_t n_docs,
+                                    const void* dq, const void* dk, int grad_dtype, const void* q,
+                                    int64_t qs, const void* k, int64_t ks, const void* wq,
+                                    const void* wk, double base, float eps, void* dqi, void* dki,
+                                    float* dwq, float* dwk, float* part, cudaStream_t st);
+// paged_append.cu.  q may be null; base 0: no rotation; eps 0: no norm.
+cudaError_t launch_paged_append(const HeadShape& s, const PagedShape& g, const void* q, int64_t qs,
+                                const void* k, int64_t ks, const void* v, int64_t vs,
+                                const void* wq, const void* wk, double base, float eps, void* kp,
+                                void* vp, void* qo, int* err, cudaStream_t st);
+
+// Attention over a paged cache.
+struct PagedAttn {
+  PagedShape g;
+  int64_t n_tok, qs;                  // packed tokens, q's token stride (elements)
+  int hq, hkv, G, tt;                 // tt: tokens of a row tile
+  float scale_log2;                   // softmax scale * log2(e)
+};
+
+size_t paged_attn_ws_bytes(const HeadShape& s);
+cudaError_t launch_paged_attn(const HeadShape& s, const PagedShape& g, int64_t max_new,
+                              float scale, const void* q, int64_t qs, const void* kp,
+                              const void* vp, void* o, float* lse, char* ws, int* err,
+                              cudaStream_t st);
+
+// Workspace of one of these operators (msa_workspace_bytes); 0 for invalid shapes.
+size_t layer_ws_bytes(const msa_params* p, int32_t op);
+
+constexpr int kPagedCtas = 160;       // most CTAs of a schedule (a B200 has 148 SMs)
+constexpr int kPagedMaxRows = 256;    // rows of the largest row tile
+
+// Workspace body: records, then (maximum, sum) and outputs of the parts.  CTA c's parts: 2c
+// (its first item) and 2c + 1 (its last, when that is another).
+struct PagedParts {
+  int4* rec;                          // [kPagedCtas] {sequence, KV head, row tile, parts}
+  float2* ml;                         // [2 * kPagedCtas][rows]
+  float* o;                           // [2 * kPagedCtas][rows][d]
+};
+
+// ------------------------------------------------------------------ device side
+struct SeqView {
+  int64_t tok0;                       // first packed token
+  int n, past, cap, n_rt;             // new tokens, tokens before them, keys there are, tiles
+};
+
+__device__ __forceinline__ SeqView load_seq(const PagedAttn& a, int s) {
+  SeqView v;
+  const int64_t c0 = max((int64_t)0, min((int64_t)__ldg(a.g.cu + s), a.n_tok));
+  const int64_t c1 = max(c0, min((int64_t)__ldg(a.g.cu + s + 1), a.n_tok));
+  const int len = __ldg(a.g.kv_lens + s);
+  const int64_t room = a.g.max_pages * a.g.page;
+  v.tok0 = c0;
+  v.n = (int)(c1 - c0);
+  v.past = len - v.n;
+  v.cap = (int)max((int64_t)0, min((int64_t)len, room));
+  v.n_rt = (v.n + a.tt - 1) / a.tt;
+  return v;
+}
+// Keys that the last token of row tile rt sees.
+__device__ __forceinline__ int tile_keys(const PagedAttn& a, const SeqView& v, int rt) {
+  const int64_t last = (int64_t)v.past + min((int64_t)v.n, (int64_t)(rt + 1) * a.tt);
+  return (int)max((int64_t)0, min(last, (int64_t)v.cap));
+}
+template <int KT>
+__device__ __forceinline__ int key_tiles(const PagedAttn& a, const SeqView& v, int rt) {
+  return max(1, (tile_keys(a, v, rt) + KT - 1) / KT);
+}
+template <int KT>
+__device__ __forceinline__ int64_t group_tiles(const PagedAttn& a, const SeqView& v) {
+  int64_t t = 0;
+  for (int rt = 0; rt < v.n_rt; ++rt) t += key_tiles<KT>(a, v, rt);
+  return t;
+}
+
+// A CTA's run of tiles and the item it starts in.
+struct Run {
+  int64_t left;                       // tiles still to do
+  int64_t share;                      // tiles of a full run
+  int s, g, rt, tile, tiles;          // current item, its next tile and its tile count
+  SeqView v;
+};
+
+struct PlanSmem {
+  int64_t warp_sum[32];
+  Run run;
+};
+
+// Every thread of the CTA calls this; the result is the same in all of them.
+template <int KT, int THREADS>
+__device__ __forceinline__ Run paged_plan(const PagedAttn& a, PlanSmem* sm) {
+  constexpr int W = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = (int)a.g.n_seqs;
+  auto tiles_of = [&](int s) -> int64_t {
+    return s < n ? group_tiles<KT>(a, load_seq(a, s)) * a.hkv : 0;
+  };
+  // total of all sequences
+  int64_t mine = tiles_of(tid);
+  int64_t sum = mine;
+  for (int s = tid + THREADS; s < n; s += THREADS) sum += tiles_of(s);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) sm->warp_sum[warp] = sum;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) total += sm->warp_sum[w];
+  const int64_t share = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x);
+  const int64_t w0 = share * blockIdx.x, w1 = min(total, w0 + share);
+  if (tid == 0) {
+    sm->run.left = 0;
+    sm->run.share = share;
+  }
+  // the sequence that holds tile w0
+  int64_t before = 0;
+  for (int s0 = 0; s0 < n && w0 < total; s0 += THREADS) {
+    if (s0 > 0) mine = tiles_of(s0 + tid);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) sm->warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t base = before;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) base += sm->warp_sum[w];
+      before += sm->warp_sum[w];
+    }
+    const int64_t lo = base + incl - mine;
+    if (w0 >= lo && w0 < lo + mine) {
+      Run r;
+      r.left = w1 - w0;
+      r.share = share;
+      r.s = s0 + tid;
+      r.v = load_seq(a, r.s);
+      int64_t rem = w0 - lo;
+      const int64_t per = mine / a.hkv;
+      r.g = (int)(rem / per);
+      rem -= r.g * per;
+      r.rt = 0;
+      while (rem >= (r.tiles = key_tiles<KT>(a, r.v, r.rt))) {
+        rem -= r.tiles;
+        ++r.rt;
+      }
+      r.tile = (int)rem;
+      sm->run = r;
+    }
+    if (before > w0) break;
+  }
+  __syncthreads();
+  return sm->run;
+}
+
+// Tiles of the current item that belong to the run.
+__device__ __forceinline__ int run_tiles(const Run& r) {
+  return (int)min((int64_t)(r.tiles - r.tile), r.left);
+}
+// Steps to the next item.  Returns false when the run is over.
+template <int KT>
+__device__ __forceinline__ bool run_next(const PagedAttn& a, Run& r) {
+  r.left -= run_tiles(r);
+  if (r.left <= 0) return false;
+  r.tile = 0;
+  if (++r.rt >= r.v.n_rt) {
+    r.rt = 0;
+    if (++r.g >= a.hkv) {
+      r.g = 0;
+      do {
+        ++r.s;
+        r.v = load_seq(a, r.s);
+      } while (r.v.n_rt == 0);
+    }
+  }
+  r.tiles = key_tiles<KT>(a, r.v, r.rt);
+  return true;
+}
+
+// Parts of an item of `tiles` tiles whose first tile is tile `at` of its CTA's run: the
+// runs it reaches into.
+__device__ __forceinline__ int item_parts(int64_t at, int64_t tiles, int64_t share) {
+  return (int)((at + tiles + share - 1) / share);
+}
+
+// The page of key `key` of a sequence, -1 (and the error bit) when the table holds none.
+__device__ __forceinline__ int key_page(const PagedAttn& a, int s, int key, int* err) {
+  const int pg = __ldg(a.g.table + (int64_t)s * a.g.max_pages + key / (int)a.g.page);
+  if (pg >= 0 && pg < a.g.n_pages) return pg;
+  set_device_error(err, MSA_DEVERR_PAGE_RANGE);
+  return -1;
+}
+
+}  // namespace msa

@@ -95,12 +95,16 @@ typedef enum {
   MSA_OP_PREFILL_MIN = 5,     /* smallest workspace msa_prefill_fwd accepts */
   MSA_OP_DECODE_OFFLOAD = 6,  /* msa_decode_fwd_offload */
   MSA_OP_SPARSE_ATTN_BWD = 7, /* msa_sparse_attn_bwd, recommended */
-  MSA_OP_SPARSE_ATTN_BWD_MIN = 8  /* smallest workspace msa_sparse_attn_bwd accepts */
+  MSA_OP_SPARSE_ATTN_BWD_MIN = 8, /* smallest workspace msa_sparse_attn_bwd accepts */
+  MSA_OP_QK_NORM_ROPE_BWD = 9,    /* msa_qk_norm_rope_bwd (with weight gradients) */
+  MSA_OP_PAGED_APPEND = 10,       /* msa_paged_append: the error word alone */
+  MSA_OP_PAGED_ATTN = 11          /* msa_paged_attn_fwd; also large enough for the append */
 } msa_op;
 
 /* Device error bits (msa_read_device_error). */
 #define MSA_DEVERR_IDX_RANGE 0x1   /* an idx entry outside [-1, nb) or violating causality */
 #define MSA_DEVERR_TIMEOUT 0x2     /* a bounded barrier wait ran out */
+#define MSA_DEVERR_PAGE_RANGE 0x4  /* a token whose page table entry is not a page of the pool */
 
 typedef struct {
   int64_t batch; /* independent sequences (prefill); ignored by decode */
@@ -208,6 +212,102 @@ MSA_API msa_status msa_prefill_fwd(const msa_params* p, const void* q, const voi
 MSA_API msa_status msa_rope_docwise(const msa_params* p, const int32_t* cu_seqlens,
                                     int64_t n_docs, void* q, void* k, double base,
                                     msa_stream_t stream);
+
+/* Per-head RMS norm of queries and keys with the document-wise rotation in the same pass,
+ * for the T = p->batch * p->seq packed tokens ([MSA-DE] names the rotation; the norm is that
+ * of models which normalise each query and key head before it):
+ *   r = (mean(x^2) + eps)^(-1/2),  n = r x w,  out = R(pos) n        per head x of d elements,
+ * pos, R and cu_seqlens as in msa_rope_docwise; a token that no document holds gets pos 0.
+ *   q, k          token t's heads at q + t * q_stride and k + t * k_stride (elements; 0 = packed,
+ *                 hq * d and hkv * d), heads d apart: views of one fused projection are taken
+ *                 as they are.  Strides are multiples of 16 bytes.
+ *   wq, wk [d]    weights in the tensors' dtype; NULL = ones.
+ *   q_out, k_out  [T, hq, d], [T, hkv, d] packed.  They may be q and k themselves where those
+ *                 are packed, and may not overlap them otherwise.
+ * eps > 0, base > 1.  Norm and rotation in fp32 (angles in fp64), rounded once.  Any
+ * hq / hkv up to 64; d 64 or 128. */
+MSA_API msa_status msa_qk_norm_rope(const msa_params* p, const int32_t* cu_seqlens,
+                                    int64_t n_docs, const void* q, int64_t q_stride,
+                                    const void* k, int64_t k_stride, const void* wq,
+                                    const void* wk, double base, float eps, void* q_out,
+                                    void* k_out, msa_stream_t stream);
+
+/* Gradient of msa_qk_norm_rope.  dq_out [T, hq, d], dk_out [T, hkv, d]: the upstream gradients,
+ * packed, of grad_dtype (MSA_F32, as msa_sparse_attn_bwd writes them, or p->dtype); q, k, wq,
+ * wk, base, eps and cu_seqlens as in the forward (nothing else is kept from it).  With
+ * g = R(pos)^T dout and u = g w:
+ *   dq, dk    [T, hq, d], [T, hkv, d] packed, p->dtype: r (u - r^2 x mean(u x));
+ *   dwq, dwk  [d] fp32: sum over tokens and heads of g r x (each may be NULL; zero for T = 0).
+ * dq and dk may not overlap the inputs.  ws: msa_workspace_bytes(p, MSA_OP_QK_NORM_ROPE_BWD, 0),
+ * needed only with dwq or dwk. */
+MSA_API msa_status msa_qk_norm_rope_bwd(const msa_params* p, const int32_t* cu_seqlens,
+                                        int64_t n_docs, const void* dq_out, const void* dk_out,
+                                        int32_t grad_dtype, const void* q, int64_t q_stride,
+                                        const void* k, int64_t k_stride, const void* wq,
+                                        const void* wk, double base, float eps, void* dq,
+                                        void* dk, float* dwq, float* dwk, void* ws,
+                                        size_t ws_bytes, msa_stream_t stream);
+
+/* A paged key/value cache and the new tokens of one step, for msa_paged_append and
+ * msa_paged_attn_fwd (the layers that a model keeps on full attention beside the sparse ones:
+ * [MoBA] switches between the two).  With p->batch sequences, p->seq = T packed new tokens and
+ * p->block tokens a page (a multiple of 16):
+ *   k_pages, v_pages  pools [n_pages, hkv, block, d] of p->dtype;
+ *   page_table        DEVICE int32 [batch, max_pages]: token i of sequence s is row i % block
+ *                     of page page_table[s][i / block];
+ *   kv_lens           DEVICE int32 [batch]: tokens of each sequence, the new ones included;
+ *   cu_seqlens        DEVICE int32 [batch + 1], nondecreasing from 0: the new tokens of
+ *                     sequence s are packed tokens cu_seqlens[s] .. cu_seqlens[s + 1] - 1, its
+ *                     last ones (none is fine).  Packed tokens from cu_seqlens[batch] to T - 1
+ *                     belong to nobody: their outputs are left as they are.
+ * The table, the lengths and the boundaries are read on the device: a captured graph replays
+ * with what they hold then.  Other contents give meaningless results but no access outside
+ * the pools and the table. */
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  const int32_t* page_table;
+  const int32_t* kv_lens;
+  const int32_t* cu_seqlens;
+  int64_t n_pages;   /* pages of each pool */
+  int64_t max_pages; /* entries of a page table row */
+} msa_paged_cache;
+
+/* Appends the step's tokens to the cache, with the norm and the rotation on the way.  New
+ * token i of sequence s, at position pos = kv_lens[s] - (its new tokens) + i:
+ *   k_pages[slot of pos] = R(pos) norm(k),  v_pages[slot of pos] = v,  q_out = R(pos) norm(q),
+ * R and norm as in msa_qk_norm_rope.  base = 0: no rotation; eps = 0: no norm (then wq and
+ * wk must be NULL).  q and q_out [T, hq, d] may both be NULL (keys and values alone); q_out
+ * may be q where that is packed.  q, k, v are strided as in msa_qk_norm_rope.  A token whose
+ * position has no page (outside the table row, or a table entry outside [0, n_pages)) is not
+ * stored and sets MSA_DEVERR_PAGE_RANGE; its query is still written.  No two new tokens may
+ * share a slot.  ws may be NULL (the error bits are then not kept), else at least
+ * msa_workspace_bytes(p, MSA_OP_PAGED_APPEND, 0). */
+MSA_API msa_status msa_paged_append(const msa_params* p, const msa_paged_cache* cache,
+                                    const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* v, int64_t v_stride,
+                                    const void* wq, const void* wk, double base, float eps,
+                                    void* q_out, void* ws, size_t ws_bytes,
+                                    msa_stream_t stream);
+
+/* Causal attention of the step's tokens over the cache that holds them: query head h of a
+ * token at position pos attends keys i <= pos of its sequence and KV head h / (hq / hkv),
+ *   o = sum_i softmax_i(p->scale * q . k_i) v_i.
+ *   q [T, hq, d] (token stride q_stride as above), o [T, hq, d] packed, lse [T, hq] fp32 (may
+ *   be NULL) = log sum_i exp(scale * q . k_i).
+ * A token at a negative position (kv_lens below the new tokens) sees nothing: o = 0,
+ * lse = -inf.  Keys past the page table row do not exist; those of a table entry outside
+ * [0, n_pages) read as zeros and set MSA_DEVERR_PAGE_RANGE.  Rows of a page behind the last
+ * token may hold anything, NaN included; keys and values of the sequence must be finite.
+ * max_new: the most new tokens of any sequence, as far as the host knows (0: unknown); it
+ * chooses the kernel, not the result's meaning.  A result has the same bits in every run
+ * with the same arguments; another max_new may round differently.
+ * ws: msa_workspace_bytes(p, MSA_OP_PAGED_ATTN, 0); it holds nothing between calls but the
+ * error word, and calls that overlap need one each.  hq / hkv up to 64; d 64 or 128. */
+MSA_API msa_status msa_paged_attn_fwd(const msa_params* p, const msa_paged_cache* cache,
+                                      int64_t max_new, const void* q, int64_t q_stride, void* o,
+                                      float* lse, void* ws, size_t ws_bytes,
+                                      msa_stream_t stream);
 
 /* Causal prefill of packed documents, each its own sequence ([MSA-DE] "Das Gehirn mit
  * zwei Geschwindigkeiten": documents are processed one by one): p->batch must be 1 and

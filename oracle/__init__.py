@@ -19,3 +19,6 @@ from .msa_sharded import (  # noqa: F401
 )
 from .msa_backward import attend_row_backward, prefill_backward  # noqa: F401
 from .msa_docs import doc_positions, prefill_varlen_rows, rope_angles, rope_docwise  # noqa: F401
+from .msa_layer import (  # noqa: F401
+    norm_rope, norm_rope_backward, paged_append, paged_attention, paged_positions, rotate_heads,
+)
