@@ -87,7 +87,7 @@ msa_status check_paged(const msa_params* p, const msa_paged_cache* c, HeadShape*
       !aligned(c->kv_lens, 4) || !aligned(c->page_table, 4))
     return MSA_ERR_INVALID_ARG;
   if (c->max_pages > 0 && c->page_table == nullptr) return MSA_ERR_INVALID_ARG;
-  if (c->n_pages > 0 && (c->k_pages == nullptr || c->v_pages == nullptr))
+  if (c->n_pages < 1 || c->k_pages == nullptr || c->v_pages == nullptr)
     return MSA_ERR_INVALID_ARG;
   if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16)) return MSA_ERR_INVALID_ARG;
   return MSA_OK;

@@ -60,10 +60,23 @@ struct PagedAttn {
   PagedShape g;
   int64_t n_tok, qs;                  // packed tokens, q's token stride (elements)
   int hq, hkv, G, tt;                 // tt: tokens of a row tile
+  int min_new, max_new;               // the launch takes sequences with this many new tokens
   float scale_log2;                   // softmax scale * log2(e)
 };
 
 size_t paged_attn_ws_bytes(const HeadShape& s);
+int paged_grid();                     // CTAs of a schedule: one an SM
+// Each kernel takes the sequences with a.min_new .. a.max_new new tokens, whatever their rows.
+// few: bf16, G <= 16 (split) or 64; simt: any type, G <= 64.
+cudaError_t launch_paged_few(const HeadShape& s, PagedAttn a, bool split, const void* q,
+                             const void* kp, const void* vp, void* o, float* lse,
+                             const struct PagedParts& parts, int* err, cudaStream_t st);
+cudaError_t launch_paged_simt(const HeadShape& s, PagedAttn a, int rows, const void* q,
+                              const void* kp, const void* vp, void* o, float* lse,
+                              const struct PagedParts& parts, int* err, cudaStream_t st);
+cudaError_t launch_paged_combine(const HeadShape& s, const PagedAttn& a, int grid, int rows,
+                                 const struct PagedParts& parts, void* o, float* lse,
+                                 cudaStream_t st);
 cudaError_t launch_paged_attn(const HeadShape& s, const PagedShape& g, int64_t max_new,
                               float scale, const void* q, int64_t qs, const void* kp,
                               const void* vp, void* o, float* lse, char* ws, int* err,
@@ -99,7 +112,7 @@ __device__ __forceinline__ SeqView load_seq(const PagedAttn& a, int s) {
   v.n = (int)(c1 - c0);
   v.past = len - v.n;
   v.cap = (int)max((int64_t)0, min((int64_t)len, room));
-  v.n_rt = (v.n + a.tt - 1) / a.tt;
+  v.n_rt = v.n < a.min_new || v.n > a.max_new ? 0 : (v.n + a.tt - 1) / a.tt;
   return v;
 }
 // Keys that the last token of row tile rt sees.

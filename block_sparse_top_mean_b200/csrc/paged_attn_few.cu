@@ -1,0 +1,413 @@
+// Attention of a few new tokens over a paged cache, bf16 (see paged.cuh for the schedule).
+//
+// With R = new tokens x G rows against a cache, 4 R flops come with every element of K and V:
+// up to R of about 64 the cache's stream from HBM is the bound, and the kernel is built round
+// it.  A producer warp walks the CTA's run of (row tile, 32-key tile) pairs and copies each
+// tile's K and V rows by tensor maps over the pools (128-byte swizzle, one box for every run of
+// keys that a page holds) into a ring of stages; page numbers are fetched 32 pieces ahead.
+// Four consumer warps run both products on mma.sync m16n8k16 (rows padded to 16: the tensor
+// pipe is far from its limit at these row counts, and a tcgen05 tile would be 128 rows):
+//   SPLIT (R <= 16): a tile belongs to one warp, so four tiles are in work at a time and a
+//     tile takes one pass of the softmax; the warps' outputs are joined in shared memory when
+//     the item ends.  Weights go into the product with V as two bf16 terms (hi + lo, 2^-17):
+//     the second product hides behind HBM, and the output is off by its own rounding alone.
+//   otherwise: a warp owns 16 of 64 rows and reads every tile; weights are rounded to bf16 once
+//     (2^-9 of each, as elsewhere in this library; 64 rows x two terms would no longer hide).
+// Keys behind the last visible one are not loaded past their page piece; their scores are
+// replaced, and their V rows (which may hold anything) masked in the fragments.
+#include "paged.cuh"
+#include "fastmath.cuh"
+#include "sm100.cuh"
+
+namespace msa {
+namespace {
+
+using namespace sm100;
+using fastmath::fast_exp2;
+
+constexpr int KT = 32;                // keys of a tile
+constexpr int kConsumers = 4;         // warps 0-3; warp 4 produces
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kHalf = KT * 128;  // 32 keys x 64 dims
+template <int D> constexpr int kStages = D == 128 ? 10 : 20;
+template <int D> constexpr uint32_t kTileBytes = KT * D * 2;
+template <int D> constexpr uint32_t kStageBytes = 2 * kTileBytes<D>;
+
+template <int D>
+struct __align__(16) Shared {
+  float o[kConsumers][16][D + 4];     // the warps' outputs of an item (SPLIT)
+  float2 ml[kConsumers][16];
+  uint64_t full[kStages<D>], empty[kStages<D>];
+  int abort;
+  PlanSmem plan;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+// C[16x8] += A[16x16] B[16x8]; thread (g, t) = (lane / 4, lane % 4) holds C rows g, g + 8 and
+// columns 2t, 2t + 1.
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Byte offset of 16-byte chunk c (8 dims each) of key row r inside a K or V tile.
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+  return (uint32_t)(c >> 3) * kHalf + (uint32_t)r * 128u + ((uint32_t)((c & 7) ^ (r & 7)) << 4);
+}
+// Clears the bf16 lanes of a fragment word whose keys (k, k + 1) are not below lim.
+__device__ __forceinline__ uint32_t keep_keys(uint32_t w, int k, int lim) {
+  return k + 1 < lim ? w : k < lim ? w & 0xffffu : 0u;
+}
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
+}
+
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attn_few_kernel(const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, int box,
+                      const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ o,
+                      float* __restrict__ lse, PagedParts parts, int* err,
+                      const __grid_constant__ PagedAttn a) {
+  constexpr int ROWS = SPLIT ? 16 : 64;
+  constexpr int ST = kStages<D>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* ring = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Shared<D>& sm = *reinterpret_cast<Shared<D>*>(ring + ST * kStageBytes<D>);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], SPLIT ? 1 : kConsumers);
+    }
+    sm.abort = 0;
+    fence_mbar_init();
+    parts.rec[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+  Run r = paged_plan<KT, kThreads>(a, &sm.plan);          // synchronises the CTA
+  if (r.left <= 0) return;
+  volatile int* abort_flag = &sm.abort;
+  auto fail = [&]() { set_device_error(err, MSA_DEVERR_TIMEOUT); *abort_flag = 1; };
+
+  if (warp == kConsumers) {
+    // ------------------------------------------------------------ producer
+    const int per = KT / box;                             // page pieces of a tile
+    if (lane == 0) {
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+    }
+    const int rows = (int)(a.g.n_pages * a.hkv * a.g.page);
+    int64_t step = 0;
+    bool ok = true;
+    do {
+      const int nt = run_tiles(r), vis = tile_keys(a, r.v, r.rt);
+      // row of piece i of the item's part of this run in the pools, `rows` (reads as zeros)
+      // for an entry that is no page, -1 past the last visible key
+      auto piece_row = [&](int i) -> int {
+        const int key = r.tile * KT + i * box;
+        if (i >= nt * per || key >= vis) return -1;
+        const int pg = key_page(a, r.s, key, err);
+        return pg < 0 ? rows : (int)(((int64_t)pg * a.hkv + r.g) * a.g.page + key % (int)a.g.page);
+      };
+      int cur = piece_row(lane), nxt = piece_row(32 + lane);
+      for (int it = 0; it < nt; ++it, ++step) {
+        const int at = it * per;                          // first piece of the tile
+        if (at > 0 && at % 32 == 0) {
+          cur = nxt;
+          nxt = piece_row(at + 32 + lane);
+        }
+        const int st = (int)(step % ST);
+        if (step >= ST && !mbar_wait_warp(&sm.empty[st], (uint32_t)((step / ST) - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        const int y = __shfl_sync(0xffffffffu, cur, (at & 31) + (lane < per ? lane : 0));
+        const bool mine = lane < per && y >= 0;
+        const int n = __popc(__ballot_sync(0xffffffffu, mine));
+        if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], (uint32_t)(n * box * D * 4));
+        __syncwarp();
+        if (mine) {
+          unsigned char* dst = ring + st * kStageBytes<D> + lane * box * 128;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+            tma_load_2d(dst + h * kHalf, &tm_k, &sm.full[st], h * 64, y);
+            tma_load_2d(dst + kTileBytes<D> + h * kHalf, &tm_v, &sm.full[st], h * 64, y);
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) ok = false;
+    } while (ok && run_next<KT>(a, r));
+    if (!ok) {
+      if (lane == 0) fail();
+      // no copy may still be landing when the CTA ends
+      for (int64_t s = step > ST ? step - ST : 0; s < step; ++s)
+        mbar_wait_warp(&sm.full[s % ST], (uint32_t)(s / ST) & 1);
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------ consumers
+  const int gr = lane >> 2, t4 = lane & 3, mi = lane >> 3, ri = lane & 7;
+  const int row0 = SPLIT ? gr : warp * 16 + gr;           // this thread's rows: row0, row0 + 8
+  int64_t step = 0;
+  bool first_item = true, aborted = false;
+  do {
+    const int nt = run_tiles(r), vis = tile_keys(a, r.v, r.rt);
+    int see[2];
+    bool there[2];                                        // rows that hold a query
+    uint32_t qa[D / 16][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = row0 + 8 * i, t_in = r.rt * a.tt + row / a.G;
+      const bool on = row < a.tt * a.G && t_in < r.v.n;
+      there[i] = on;
+      see[i] = on ? (int)max(0LL, min((long long)r.v.past + t_in + 1, (long long)r.v.cap)) : 0;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          q + (r.v.tok0 + t_in) * a.qs + (int64_t)(r.g * a.G + row % a.G) * D);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        qa[ks][i] = on ? __ldg(src + ks * 8 + t4) : 0u;
+        qa[ks][2 + i] = on ? __ldg(src + ks * 8 + 4 + t4) : 0u;
+      }
+    }
+    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+    float acc[D / 8][4];
+#pragma unroll
+    for (int dt = 0; dt < D / 8; ++dt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[dt][e] = 0.f;
+
+    for (int it = 0; it < nt; ++it, ++step) {
+      if (SPLIT && (int)(step % kConsumers) != warp) continue;
+      const int st = (int)(step % ST);
+      if (aborted || __any_sync(0xffffffffu, *abort_flag != 0)) { aborted = true; continue; }
+      if (!mbar_wait_warp(&sm.full[st], (uint32_t)(step / ST) & 1)) {
+        if (lane == 0) fail();
+        aborted = true;
+        continue;
+      }
+      const uint32_t sk = smem_u32(ring + st * kStageBytes<D>), sv = sk + kTileBytes<D>;
+      const int key0 = (r.tile + it) * KT;
+      float s[KT / 8][4];
+#pragma unroll
+      for (int nt8 = 0; nt8 < KT / 8; ++nt8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt8][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ks += 2)
+#pragma unroll
+        for (int nt8 = 0; nt8 < KT / 8; ++nt8) {
+          uint32_t b[4];
+          ldsm4(sk + tile_off(nt8 * 8 + ri, 2 * ks + mi), b);
+          mma16816(s[nt8], qa[ks], b[0], b[1]);
+          mma16816(s[nt8], qa[ks + 1], b[2], b[3]);
+        }
+      // online softmax of rows row0 and row0 + 8 over the tile's 32 keys
+      // (rows that hold no query need no mask: their results go nowhere)
+      const bool inside = __all_sync(0xffffffffu, (!there[0] || key0 + KT <= see[0]) &&
+                                                      (!there[1] || key0 + KT <= see[1]));
+      float ref[2], alpha[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = -CUDART_INF_F;
+#pragma unroll
+        for (int nt8 = 0; nt8 < KT / 8; ++nt8)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = s[nt8][2 * i + e] * a.scale_log2;
+            if (!inside && key0 + nt8 * 8 + 2 * t4 + e >= see[i]) x = -CUDART_INF_F;
+            s[nt8][2 * i + e] = x;
+            mx = fmaxf(mx, x);
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[i], mx);
+        ref[i] = mn == -CUDART_INF_F ? 0.f : mn;
+        alpha[i] = fast_exp2(m[i] - ref[i]);
+        m[i] = mn;
+        float add = 0.f;
+#pragma unroll
+        for (int nt8 = 0; nt8 < KT / 8; ++nt8)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float p = fast_exp2(s[nt8][2 * i + e] - ref[i]);
+            s[nt8][2 * i + e] = p;
+            add += p;
+          }
+        l[i] = l[i] * alpha[i] + add;
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int dt = 0; dt < D / 8; ++dt) {
+          acc[dt][0] *= alpha[0];
+          acc[dt][1] *= alpha[0];
+          acc[dt][2] *= alpha[1];
+          acc[dt][3] *= alpha[1];
+        }
+      }
+      const int lim = vis - key0;                         // keys of the tile that exist
+#pragma unroll
+      for (int kk = 0; kk < KT / 16; ++kk) {
+        uint32_t ph[4], pl[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {                     // (row, key half): (0,0) (1,0) (0,1) (1,1)
+          const float p0 = s[2 * kk + (w >> 1)][2 * (w & 1)];
+          const float p1 = s[2 * kk + (w >> 1)][2 * (w & 1) + 1];
+          ph[w] = pack_bf16x2(p0, p1);
+          if (SPLIT)
+            pl[w] = pack_bf16x2(p0 - bf16lo_to_f32(ph[w]), p1 - bf16hi_to_f32(ph[w]));
+        }
+#pragma unroll
+        for (int dt = 0; dt < D / 8; dt += 2) {
+          uint32_t b[4];
+          ldsm4_t(sv + tile_off(kk * 16 + (mi & 1) * 8 + ri, dt + (mi >> 1)), b);
+          if (lim < KT) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) b[w] = keep_keys(b[w], kk * 16 + (w & 1) * 8 + 2 * t4, lim);
+          }
+          mma16816(acc[dt], ph, b[0], b[1]);
+          mma16816(acc[dt + 1], ph, b[2], b[3]);
+          if (SPLIT) {
+            mma16816(acc[dt], pl, b[0], b[1]);
+            mma16816(acc[dt + 1], pl, b[2], b[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[st]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+    const bool whole = r.tile == 0 && nt == r.tiles;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (first_item ? 0 : 1);
+    if (SPLIT) {
+      // join the four warps: thread = (row tid / 8, D / 8 columns)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (t4 == 0) sm.ml[warp][gr + 8 * i] = make_float2(m[i], l[i]);
+#pragma unroll
+        for (int dt = 0; dt < D / 8; ++dt)
+          *reinterpret_cast<float2*>(&sm.o[warp][gr + 8 * i][dt * 8 + 2 * t4]) =
+              make_float2(acc[dt][2 * i], acc[dt][2 * i + 1]);
+      }
+      consumers_sync();
+      const int row = tid / 8, c0 = (tid % 8) * 4, t_in = r.rt * a.tt + row / a.G;
+      const bool on = row < a.tt * a.G && t_in < r.v.n;
+      float mx = -CUDART_INF_F, sum = 0.f, w[kConsumers];
+#pragma unroll
+      for (int i = 0; i < kConsumers; ++i) mx = fmaxf(mx, sm.ml[i][row].x);
+      const float base = mx == -CUDART_INF_F ? 0.f : mx;
+#pragma unroll
+      for (int i = 0; i < kConsumers; ++i) {
+        w[i] = fast_exp2(sm.ml[i][row].x - base);
+        sum = fmaf(sm.ml[i][row].y, w[i], sum);
+      }
+      const float inv = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+      const int64_t qrow = (r.v.tok0 + t_in) * a.hq + r.g * a.G + row % a.G;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const int c = j * 32 + c0;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kConsumers; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(&sm.o[i][row][c]);
+          y.x = fmaf(x.x, w[i], y.x);
+          y.y = fmaf(x.y, w[i], y.y);
+          y.z = fmaf(x.z, w[i], y.z);
+          y.w = fmaf(x.w, w[i], y.w);
+        }
+        if (!on) continue;
+        if (whole) {
+          *reinterpret_cast<uint2*>(o + qrow * D + c) =
+              make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+        } else {
+          *reinterpret_cast<float4*>(parts.o + (slot * ROWS + row) * D + c) = y;
+        }
+      }
+      if (on && tid % 8 == 0) {
+        if (!whole) parts.ml[slot * ROWS + row] = make_float2(mx, sum);
+        else if (lse != nullptr) lse[qrow] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -CUDART_INF_F;
+      }
+      consumers_sync();
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = row0 + 8 * i, t_in = r.rt * a.tt + row / a.G;
+        if (row >= a.tt * a.G || t_in >= r.v.n) continue;
+        const int64_t qrow = (r.v.tok0 + t_in) * a.hq + r.g * a.G + row % a.G;
+        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+#pragma unroll
+        for (int dt = 0; dt < D / 8; ++dt) {
+          const float x = acc[dt][2 * i], y = acc[dt][2 * i + 1];
+          const int c = dt * 8 + 2 * t4;
+          if (whole)
+            *reinterpret_cast<uint32_t*>(o + qrow * D + c) = pack_bf16x2(x * inv, y * inv);
+          else
+            *reinterpret_cast<float2*>(parts.o + (slot * ROWS + row) * D + c) = make_float2(x, y);
+        }
+        if (t4 == 0) {
+          if (!whole) parts.ml[slot * ROWS + row] = make_float2(m[i], l[i]);
+          else if (lse != nullptr)
+            lse[qrow] = l[i] > 0.f ? (m[i] + log2f(l[i])) * kLn2 : -CUDART_INF_F;
+        }
+      }
+    }
+    if (!whole && r.tile == 0 && tid == 0)
+      parts.rec[blockIdx.x] = make_int4(r.s, r.g, r.rt | (first_item ? 0 : 1 << 30),
+                                        item_parts(r.share - r.left, r.tiles, r.share));
+    first_item = false;
+  } while (run_next<KT>(a, r));
+}
+
+template <int D, bool SPLIT>
+cudaError_t run(PagedAttn& a, const HeadShape& s, const void* q, const void* kp, const void* vp,
+                void* o, float* lse, const PagedParts& parts, int* err, cudaStream_t st) {
+  constexpr int ROWS = SPLIT ? 16 : 64;
+  a.tt = ROWS / a.G;
+  const int box = a.g.page % 32 == 0 ? 32 : 16;           // keys of one copy: they share a page
+  const int64_t rows = a.g.n_pages * a.hkv * a.g.page;
+  CUtensorMap mk{}, mv{};
+  if (rows > 0 && (!make_bf16_2d_map(&mk, kp, rows, D, box) ||
+                   !make_bf16_2d_map(&mv, vp, rows, D, box)))
+    return cudaErrorInvalidValue;
+  const size_t smem = 1024 + kStages<D> * kStageBytes<D> + sizeof(Shared<D>);
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_few_kernel<D, SPLIT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int grid = paged_grid();
+  paged_attn_few_kernel<D, SPLIT><<<grid, kThreads, smem, st>>>(
+      mk, mv, box, (const __nv_bfloat16*)q, (__nv_bfloat16*)o, lse, parts, err, a);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? launch_paged_combine(s, a, grid, ROWS, parts, o, lse, st) : e;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_few(const HeadShape& s, PagedAttn a, bool split, const void* q,
+                             const void* kp, const void* vp, void* o, float* lse,
+                             const PagedParts& parts, int* err, cudaStream_t st) {
+  if (s.d == 128)
+    return split ? run<128, true>(a, s, q, kp, vp, o, lse, parts, err, st)
+                 : run<128, false>(a, s, q, kp, vp, o, lse, parts, err, st);
+  return split ? run<64, true>(a, s, q, kp, vp, o, lse, parts, err, st)
+               : run<64, false>(a, s, q, kp, vp, o, lse, parts, err, st);
+}
+
+}  // namespace msa

@@ -150,110 +150,31 @@ paged_attn_simt_kernel(const T* __restrict__ q, const T* __restrict__ kp,
   } while (run_next<KT>(a, r));
 }
 
-// Joins the parts of the item that CTA blockIdx.x began and did not finish: one warp a row.
-template <typename T, int D>
-__global__ void __launch_bounds__(128)
-paged_combine_kernel(PagedParts parts, int rows, T* __restrict__ o, float* __restrict__ lse,
-                     const __grid_constant__ PagedAttn a) {
-  const int4 rec = parts.rec[blockIdx.x];
-  if (rec.w == 0) return;
-  constexpr int E = D / 32;           // columns of a lane
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
-  const int rt = rec.z & ~(1 << 30);
-  const SeqView v = load_seq(a, rec.x);
-  const int t_in = rt * a.tt + row / a.G, h = row % a.G;
-  if (row >= rows || row >= a.tt * a.G || t_in >= v.n) return;
-  const int64_t slot0 = 2 * (int64_t)blockIdx.x + (rec.z >> 30 & 1);
-  auto slot = [&](int i) -> int64_t { return i == 0 ? slot0 : 2 * ((int64_t)blockIdx.x + i); };
-  float mx = -CUDART_INF_F;
-  for (int i = lane; i < rec.w; i += 32) mx = fmaxf(mx, parts.ml[slot(i) * rows + row].x);
-  mx = warp_max(mx);
-  if (mx == -CUDART_INF_F) mx = 0.f;
-  float l = 0.f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < rec.w; ++i) {
-    const float2 ml = parts.ml[slot(i) * rows + row];
-    const float w = exp2f(ml.x - mx);
-    const float* src = parts.o + (slot(i) * rows + row) * D + lane * E;
-    l = fmaf(ml.y, w, l);
-    if (E == 4) {
-      const float4 y = *reinterpret_cast<const float4*>(src);
-      acc[0] = fmaf(y.x, w, acc[0]);
-      acc[1] = fmaf(y.y, w, acc[1]);
-      acc[E - 2] = fmaf(y.z, w, acc[E - 2]);
-      acc[E - 1] = fmaf(y.w, w, acc[E - 1]);
-    } else {
-      const float2 y = *reinterpret_cast<const float2*>(src);
-      acc[0] = fmaf(y.x, w, acc[0]);
-      acc[1] = fmaf(y.y, w, acc[1]);
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int64_t qrow = (v.tok0 + t_in) * a.hq + rec.y * a.G + h;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[qrow * D + lane * E + e] = from_f32<T>(acc[e] * inv);
-  if (lane == 0 && lse != nullptr)
-    lse[qrow] = l > 0.f ? (mx + log2f(l)) * kLn2 : -CUDART_INF_F;
-}
-
 template <typename T, int D, int ROWS>
-cudaError_t run(PagedAttn& a, const void* q, const void* kp, const void* vp, void* o, float* lse,
-                char* ws, int* err, cudaStream_t st) {
-  PagedParts parts;
-  parts.rec = reinterpret_cast<int4*>(ws);
-  parts.ml = reinterpret_cast<float2*>(ws + kPagedCtas * sizeof(int4));
-  parts.o = reinterpret_cast<float*>(ws + kPagedCtas * sizeof(int4) +
-                                     (size_t)2 * kPagedCtas * kPagedMaxRows * sizeof(float2));
+cudaError_t run(PagedAttn& a, const HeadShape& s, const void* q, const void* kp, const void* vp,
+                void* o, float* lse, const PagedParts& parts, int* err, cudaStream_t st) {
   a.tt = ROWS / a.G;
   const size_t smem = sizeof(Smem<D, ROWS>);
   cudaError_t e = cudaFuncSetAttribute(paged_attn_simt_kernel<T, D, ROWS>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int grid = sm_count() < kPagedCtas ? sm_count() : kPagedCtas;
+  const int grid = paged_grid();
   paged_attn_simt_kernel<T, D, ROWS><<<grid, ROWS * kLanes, smem, st>>>(
       (const T*)q, (const T*)kp, (const T*)vp, (T*)o, lse, parts, err, a);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  paged_combine_kernel<T, D><<<dim3(grid, ROWS / 4), 128, 0, st>>>(parts, ROWS, (T*)o, lse, a);
-  return cudaGetLastError();
-}
-
-template <typename T, int D>
-cudaError_t run_rows(PagedAttn& a, int64_t max_new, const void* q, const void* kp, const void* vp,
-                     void* o, float* lse, char* ws, int* err, cudaStream_t st) {
-  if (max_new * a.G <= 16) return run<T, D, 16>(a, q, kp, vp, o, lse, ws, err, st);
-  return run<T, D, 64>(a, q, kp, vp, o, lse, ws, err, st);
+  return e == cudaSuccess ? launch_paged_combine(s, a, grid, ROWS, parts, o, lse, st) : e;
 }
 
 }  // namespace
 
-size_t paged_attn_ws_bytes(const HeadShape& s) {
-  return kPagedCtas * sizeof(int4) +
-         (size_t)2 * kPagedCtas * kPagedMaxRows * (sizeof(float2) + s.d * sizeof(float));
-}
-
-cudaError_t launch_paged_attn(const HeadShape& s, const PagedShape& g, int64_t max_new,
-                              float scale, const void* q, int64_t qs, const void* kp,
-                              const void* vp, void* o, float* lse, char* ws, int* err,
-                              cudaStream_t st) {
-  PagedAttn a{};
-  a.g = g;
-  a.n_tok = s.n_tok;
-  a.qs = qs;
-  a.hq = (int)s.hq;
-  a.hkv = (int)s.hkv;
-  a.G = (int)(s.hq / s.hkv);
-  a.scale_log2 = scale * 1.4426950408889634f;
-  if (max_new < 1 || max_new > s.n_tok) max_new = s.n_tok;
-  using B = __nv_bfloat16;
-  if (s.dtype == MSA_BF16)
-    return s.d == 128 ? run_rows<B, 128>(a, max_new, q, kp, vp, o, lse, ws, err, st)
-                      : run_rows<B, 64>(a, max_new, q, kp, vp, o, lse, ws, err, st);
-  return s.d == 128 ? run_rows<float, 128>(a, max_new, q, kp, vp, o, lse, ws, err, st)
-                    : run_rows<float, 64>(a, max_new, q, kp, vp, o, lse, ws, err, st);
+cudaError_t launch_paged_simt(const HeadShape& s, PagedAttn a, int rows, const void* q,
+                              const void* kp, const void* vp, void* o, float* lse,
+                              const PagedParts& parts, int* err, cudaStream_t st) {
+  if (s.d == 128)
+    return rows <= 16 ? run<float, 128, 16>(a, s, q, kp, vp, o, lse, parts, err, st)
+                      : run<float, 128, 64>(a, s, q, kp, vp, o, lse, parts, err, st);
+  return rows <= 16 ? run<float, 64, 16>(a, s, q, kp, vp, o, lse, parts, err, st)
+                    : run<float, 64, 64>(a, s, q, kp, vp, o, lse, parts, err, st);
 }
 
 }  // namespace msa

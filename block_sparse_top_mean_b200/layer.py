@@ -27,7 +27,8 @@ def _fail(text):
 def _call(name, device, *args):
     """The library's entry on `device`'s current stream (launches need it to be current)."""
     fn = getattr(_lib.load(), name)
-    stream = torch.cuda.current_stream(device).cuda_stream
+    # the raw handle: building a torch.cuda.Stream object costs 2 us of a 10 us call
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if torch.cuda.current_device() == device.index:
         st = fn(*args, stream)
     else:

@@ -105,7 +105,7 @@ def _cache(**kw):
 
 
 BAD_CACHES = [(dict(k=None), INVALID), (dict(v=4096 + 8), INVALID), (dict(table=None), INVALID),
-              (dict(lens=None), INVALID), (dict(cu=4097), INVALID), (dict(n=-1), INVALID),
+              (dict(lens=None), INVALID), (dict(cu=4097), INVALID), (dict(n=-1), INVALID), (dict(n=0), INVALID),
               (dict(m=-1), INVALID), (dict(n=1 << 40), UNSUPPORTED), (dict(m=1 << 40), UNSUPPORTED)]
 
 
