@@ -10,14 +10,15 @@
 // head, row tile); its key tiles are those up to its last token's position (at least one, so
 // that rows that see nothing are still written).
 //
-// Schedule.  All key tiles of all items, in order, are one line of W tiles that the CTAs cut
-// into equal runs (a run may start and end inside an item), so the work is even whatever the
-// lengths are: one long sequence, or many of very different lengths.  Every CTA finds its run
-// itself from cu and kv_lens (a scan over the sequences), so the lengths may change between
-// replays of a captured graph.  An item that one CTA holds whole is finished there; of one
-// that is cut, each CTA leaves its running maximum, sum and unnormalised output (fp32), and
-// the CTA that holds the item's first tile a record of how many parts there are.  Parts are
-// joined in order: results do not depend on timing.
+// Schedule.  An item counts as its key tiles plus `lead` (what starting and finishing an item
+// costs, in tiles).  All items, in order, are one line that the CTAs cut into equal runs (a
+// run may start and end inside an item), so the work is even whatever the lengths are: one
+// long sequence, or many of very different lengths.  Every CTA finds its run itself from cu
+// and kv_lens (a scan over the sequences), so the lengths may change between replays of a
+// captured graph.  An item that one CTA holds whole is finished there; of one that is cut,
+// each CTA leaves its running maximum, sum and unnormalised output (fp32), and the CTA that
+// holds the item's first tile a record of how many parts there are.  Parts are joined in
+// order: results do not depend on timing.
 #pragma once
 
 #include <math_constants.h>
@@ -60,6 +61,7 @@ struct PagedAttn {
   PagedShape g;
   int64_t n_tok, qs;                  // packed tokens, q's token stride (elements)
   int hq, hkv, G, tt;                 // tt: tokens of a row tile
+  int lead;                           // cost of an item beside its tiles (in tiles)
   int min_new, max_new;               // the launch takes sequences with this many new tokens
   float scale_log2;                   // softmax scale * log2(e)
 };
@@ -67,8 +69,8 @@ struct PagedAttn {
 size_t paged_attn_ws_bytes(const HeadShape& s);
 int paged_grid();                     // CTAs of a schedule: one an SM
 // Each kernel takes the sequences with a.min_new .. a.max_new new tokens, whatever their rows.
-// few: bf16, G <= 16 (split) or 64; simt: any type, G <= 64.
-cudaError_t launch_paged_few(const HeadShape& s, PagedAttn a, bool split, const void* q,
+// rows: the row tile asked for (at least G).  few: bf16; simt: fp32.
+cudaError_t launch_paged_few(const HeadShape& s, PagedAttn a, int rows, const void* q,
                              const void* kp, const void* vp, void* o, float* lse,
                              const struct PagedParts& parts, int* err, cudaStream_t st);
 cudaError_t launch_paged_simt(const HeadShape& s, PagedAttn a, int rows, const void* q,
@@ -91,7 +93,7 @@ constexpr int kPagedMaxRows = 256;    // rows of the largest row tile
 // Workspace body: records, then (maximum, sum) and outputs of the parts.  CTA c's parts: 2c
 // (its first item) and 2c + 1 (its last, when that is another).
 struct PagedParts {
-  int4* rec;                          // [kPagedCtas] {sequence, KV head, row tile, parts}
+  int4* rec;                          // [kPagedCtas], see item_record
   float2* ml;                         // [2 * kPagedCtas][rows]
   float* o;                           // [2 * kPagedCtas][rows][d]
 };
@@ -125,17 +127,18 @@ __device__ __forceinline__ int key_tiles(const PagedAttn& a, const SeqView& v, i
   return max(1, (tile_keys(a, v, rt) + KT - 1) / KT);
 }
 template <int KT>
-__device__ __forceinline__ int64_t group_tiles(const PagedAttn& a, const SeqView& v) {
-  int64_t t = 0;
+__device__ __forceinline__ int64_t group_cost(const PagedAttn& a, const SeqView& v) {
+  int64_t t = (int64_t)v.n_rt * a.lead;
   for (int rt = 0; rt < v.n_rt; ++rt) t += key_tiles<KT>(a, v, rt);
   return t;
 }
 
-// A CTA's run of tiles and the item it starts in.
+// A CTA's run [at, end) of the line and the item it is in: `tiles` tiles from `start` + lead on
+// the line.
 struct Run {
-  int64_t left;                       // tiles still to do
-  int64_t share;                      // tiles of a full run
-  int s, g, rt, tile, tiles;          // current item, its next tile and its tile count
+  int64_t at, end, start;
+  int64_t share;                      // length of a run
+  int s, g, rt, tiles;
   SeqView v;
 };
 
@@ -150,8 +153,9 @@ __device__ __forceinline__ Run paged_plan(const PagedAttn& a, PlanSmem* sm) {
   constexpr int W = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = (int)a.g.n_seqs;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // paged_combine_kernel
   auto tiles_of = [&](int s) -> int64_t {
-    return s < n ? group_tiles<KT>(a, load_seq(a, s)) * a.hkv : 0;
+    return s < n ? group_cost<KT>(a, load_seq(a, s)) * a.hkv : 0;
   };
   // total of all sequences
   int64_t mine = tiles_of(tid);
@@ -166,11 +170,8 @@ __device__ __forceinline__ Run paged_plan(const PagedAttn& a, PlanSmem* sm) {
   for (int w = 0; w < W; ++w) total += sm->warp_sum[w];
   const int64_t share = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x);
   const int64_t w0 = share * blockIdx.x, w1 = min(total, w0 + share);
-  if (tid == 0) {
-    sm->run.left = 0;
-    sm->run.share = share;
-  }
-  // the sequence that holds tile w0
+  if (tid == 0) sm->run.at = sm->run.end = 0;
+  // the sequence that holds w0
   int64_t before = 0;
   for (int s0 = 0; s0 < n && w0 < total; s0 += THREADS) {
     if (s0 > 0) mine = tiles_of(s0 + tid);
@@ -192,20 +193,20 @@ __device__ __forceinline__ Run paged_plan(const PagedAttn& a, PlanSmem* sm) {
     const int64_t lo = base + incl - mine;
     if (w0 >= lo && w0 < lo + mine) {
       Run r;
-      r.left = w1 - w0;
+      r.at = w0;
+      r.end = w1;
       r.share = share;
       r.s = s0 + tid;
       r.v = load_seq(a, r.s);
-      int64_t rem = w0 - lo;
       const int64_t per = mine / a.hkv;
-      r.g = (int)(rem / per);
-      rem -= r.g * per;
+      r.g = (int)((w0 - lo) / per);
+      r.start = lo + r.g * per;
       r.rt = 0;
-      while (rem >= (r.tiles = key_tiles<KT>(a, r.v, r.rt))) {
-        rem -= r.tiles;
-        ++r.rt;
+      r.tiles = key_tiles<KT>(a, r.v, 0);
+      while (w0 >= r.start + a.lead + r.tiles) {
+        r.start += a.lead + r.tiles;
+        r.tiles = key_tiles<KT>(a, r.v, ++r.rt);
       }
-      r.tile = (int)rem;
       sm->run = r;
     }
     if (before > w0) break;
@@ -214,16 +215,21 @@ __device__ __forceinline__ Run paged_plan(const PagedAttn& a, PlanSmem* sm) {
   return sm->run;
 }
 
-// Tiles of the current item that belong to the run.
-__device__ __forceinline__ int run_tiles(const Run& r) {
-  return (int)min((int64_t)(r.tiles - r.tile), r.left);
+// First tile of the current item that belongs to the run, and how many do (none when the run
+// ends in the item's lead).
+__device__ __forceinline__ int run_first(const PagedAttn& a, const Run& r) {
+  return (int)max((int64_t)0, r.at - r.start - a.lead);
+}
+__device__ __forceinline__ int run_tiles(const PagedAttn& a, const Run& r) {
+  const int64_t to = min((int64_t)r.tiles, r.end - r.start - a.lead);
+  return (int)max((int64_t)0, to - run_first(a, r));
 }
 // Steps to the next item.  Returns false when the run is over.
 template <int KT>
 __device__ __forceinline__ bool run_next(const PagedAttn& a, Run& r) {
-  r.left -= run_tiles(r);
-  if (r.left <= 0) return false;
-  r.tile = 0;
+  r.start += a.lead + r.tiles;
+  if (r.start >= r.end) return false;
+  r.at = r.start;
   if (++r.rt >= r.v.n_rt) {
     r.rt = 0;
     if (++r.g >= a.hkv) {
@@ -238,10 +244,19 @@ __device__ __forceinline__ bool run_next(const PagedAttn& a, Run& r) {
   return true;
 }
 
-// Parts of an item of `tiles` tiles whose first tile is tile `at` of its CTA's run: the
-// runs it reaches into.
-__device__ __forceinline__ int item_parts(int64_t at, int64_t tiles, int64_t share) {
-  return (int)((at + tiles + share - 1) / share);
+// Runs that the current item's tiles reach into.
+__device__ __forceinline__ int item_parts(const PagedAttn& a, const Run& r) {
+  const int64_t first = r.start + a.lead;
+  return (int)((first + r.tiles - 1) / r.share - first / r.share) + 1;
+}
+
+// The record of a cut item: row of its first query in o and lse (low and high word), its
+// tokens << 1 | which of the CTA's two parts it is, and the number of parts.
+__device__ __forceinline__ int4 item_record(const PagedAttn& a, const Run& r, bool first_item) {
+  const int64_t row = (r.v.tok0 + (int64_t)r.rt * a.tt) * a.hq + r.g * a.G;
+  const int toks = min(a.tt, r.v.n - r.rt * a.tt);
+  return make_int4((int)(row & 0xffffffff), (int)(row >> 32), toks << 1 | (first_item ? 0 : 1),
+                   item_parts(a, r));
 }
 
 // The page of key `key` of a sequence, -1 (and the error bit) when the table holds none.

@@ -7,53 +7,87 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Joins the parts of the item that CTA blockIdx.x began and did not finish: one warp a row.
-template <typename T, int D>
-__global__ void __launch_bounds__(128)
+// Joins the parts of the item that CTA blockIdx.x began and did not finish.  WARPS warps a
+// row, each over every WARPS-th part, joined in order; the parts come from L2, so what counts
+// is the chain record -> maxima -> outputs, and that it starts while the attention kernel
+// still runs (programmatic dependent launch: the wait below is for that kernel's results).
+template <typename T, int D, int WARPS>
+__global__ void __launch_bounds__(256)
 paged_combine_kernel(PagedParts parts, int rows, T* __restrict__ o, float* __restrict__ lse,
-                     const __grid_constant__ PagedAttn a) {
-  const int4 rec = parts.rec[blockIdx.x];
-  if (rec.w == 0) return;
+                     int G, int hq) {
   constexpr int E = D / 32;           // columns of a lane
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
-  const int rt = rec.z & ~(1 << 30);
-  const SeqView v = load_seq(a, rec.x);
-  const int t_in = rt * a.tt + row / a.G, h = row % a.G;
-  if (row >= rows || row >= a.tt * a.G || t_in >= v.n) return;
-  const int64_t slot0 = 2 * (int64_t)blockIdx.x + (rec.z >> 30 & 1);
+  constexpr int RB = 8 / WARPS;       // rows of a block
+  __shared__ float s_acc[8][D];
+  __shared__ float s_l[8];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 rec = parts.rec[blockIdx.x];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wr = warp % WARPS;
+  const int row = blockIdx.y * RB + warp / WARPS;
+  if (rec.w == 0 || (int)(blockIdx.y * RB) >= (rec.z >> 1) * G) return;   // whole block
+  const bool on = row < (rec.z >> 1) * G;
+  const int n = on ? rec.w : 0;
+  const int64_t slot0 = 2 * (int64_t)blockIdx.x + (rec.z & 1);
   auto slot = [&](int i) -> int64_t { return i == 0 ? slot0 : 2 * ((int64_t)blockIdx.x + i); };
   float mx = -CUDART_INF_F;
-  for (int i = lane; i < rec.w; i += 32) mx = fmaxf(mx, parts.ml[slot(i) * rows + row].x);
+  for (int i = lane; i < n; i += 32) mx = fmaxf(mx, parts.ml[slot(i) * rows + row].x);
   mx = warp_max(mx);
-  if (mx == -CUDART_INF_F) mx = 0.f;
+  const float ref = mx == -CUDART_INF_F ? 0.f : mx;
   float l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-  for (int i = 0; i < rec.w; ++i) {
+  for (int i = wr; i < n; i += WARPS) {
     const float2 ml = parts.ml[slot(i) * rows + row];
-    const float w = exp2f(ml.x - mx);
     const float* src = parts.o + (slot(i) * rows + row) * D + lane * E;
+    float y[E];
+    if (E == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(src);
+    else *reinterpret_cast<float2*>(y) = *reinterpret_cast<const float2*>(src);
+    const float w = exp2f(ml.x - ref);
     l = fmaf(ml.y, w, l);
-    if (E == 4) {
-      const float4 y = *reinterpret_cast<const float4*>(src);
-      acc[0] = fmaf(y.x, w, acc[0]);
-      acc[1] = fmaf(y.y, w, acc[1]);
-      acc[E - 2] = fmaf(y.z, w, acc[E - 2]);
-      acc[E - 1] = fmaf(y.w, w, acc[E - 1]);
-    } else {
-      const float2 y = *reinterpret_cast<const float2*>(src);
-      acc[0] = fmaf(y.x, w, acc[0]);
-      acc[1] = fmaf(y.y, w, acc[1]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(y[e], w, acc[e]);
+  }
+  if (WARPS > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (wr != 0) return;
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) {
+      l += s_l[warp + w];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += s_acc[warp + w][lane * E + e];
     }
   }
+  if (!on) return;
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int64_t qrow = (v.tok0 + t_in) * a.hq + rec.y * a.G + h;
+  const int64_t qrow = ((int64_t)rec.y << 32 | (uint32_t)rec.x) + (int64_t)(row / G) * hq + row % G;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[qrow * D + lane * E + e] = from_f32<T>(acc[e] * inv);
   if (lane == 0 && lse != nullptr)
     lse[qrow] = l > 0.f ? (mx + log2f(l)) * kLn2 : -CUDART_INF_F;
+}
+
+template <typename T, int D>
+cudaError_t run_combine(const PagedAttn& a, int grid, int rows, const PagedParts& parts, void* o,
+                        float* lse, cudaStream_t st) {
+  // few rows may have a part from every CTA: eight warps a row; large row tiles have few parts
+  const bool few = rows <= 16;
+  const int used = a.tt * a.G;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, few ? used : (used + 7) / 8);
+  cfg.blockDim = 256;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return few ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, D, 8>, parts, rows, (T*)o, lse,
+                                  a.G, a.hq)
+             : cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, D, 1>, parts, rows, (T*)o, lse,
+                                  a.G, a.hq);
 }
 
 PagedParts parts_of(char* ws) {
@@ -76,18 +110,12 @@ int paged_grid() { return sm_count() < kPagedCtas ? sm_count() : kPagedCtas; }
 
 cudaError_t launch_paged_combine(const HeadShape& s, const PagedAttn& a, int grid, int rows,
                                  const PagedParts& parts, void* o, float* lse, cudaStream_t st) {
-  const dim3 g(grid, (a.tt * a.G + 3) / 4);
   using B = __nv_bfloat16;
-  if (s.dtype == MSA_BF16) {
-    if (s.d == 128) paged_combine_kernel<B, 128><<<g, 128, 0, st>>>(parts, rows, (B*)o, lse, a);
-    else paged_combine_kernel<B, 64><<<g, 128, 0, st>>>(parts, rows, (B*)o, lse, a);
-  } else {
-    if (s.d == 128)
-      paged_combine_kernel<float, 128><<<g, 128, 0, st>>>(parts, rows, (float*)o, lse, a);
-    else
-      paged_combine_kernel<float, 64><<<g, 128, 0, st>>>(parts, rows, (float*)o, lse, a);
-  }
-  return cudaGetLastError();
+  if (s.dtype == MSA_BF16)
+    return s.d == 128 ? run_combine<B, 128>(a, grid, rows, parts, o, lse, st)
+                      : run_combine<B, 64>(a, grid, rows, parts, o, lse, st);
+  return s.d == 128 ? run_combine<float, 128>(a, grid, rows, parts, o, lse, st)
+                    : run_combine<float, 64>(a, grid, rows, parts, o, lse, st);
 }
 
 cudaError_t launch_paged_attn(const HeadShape& s, const PagedShape& g, int64_t max_new,
@@ -109,7 +137,7 @@ cudaError_t launch_paged_attn(const HeadShape& s, const PagedShape& g, int64_t m
   const PagedParts parts = parts_of(ws);
   if (s.dtype == MSA_F32)
     return launch_paged_simt(s, a, rows <= 16 ? 16 : 64, q, kp, vp, o, lse, parts, err, st);
-  return launch_paged_few(s, a, rows <= 16, q, kp, vp, o, lse, parts, err, st);
+  return launch_paged_few(s, a, rows <= 16 ? (int)rows : 64, q, kp, vp, o, lse, parts, err, st);
 }
 
 }  // namespace msa

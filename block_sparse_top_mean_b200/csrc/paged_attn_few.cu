@@ -1,18 +1,22 @@
 // Attention of a few new tokens over a paged cache, bf16 (see paged.cuh for the schedule).
 //
 // With R = new tokens x G rows against a cache, 4 R flops come with every element of K and V:
-// up to R of about 64 the cache's stream from HBM is the bound, and the kernel is built round
+// up to R of about 64 the cache's stream from HBM is the bound, and the kernels are built round
 // it.  A producer warp walks the CTA's run of (row tile, 32-key tile) pairs and copies each
 // tile's K and V rows by tensor maps over the pools (128-byte swizzle, one box for every run of
 // keys that a page holds) into a ring of stages; page numbers are fetched 32 pieces ahead.
-// Four consumer warps run both products on mma.sync m16n8k16 (rows padded to 16: the tensor
-// pipe is far from its limit at these row counts, and a tcgen05 tile would be 128 rows):
-//   SPLIT (R <= 16): a tile belongs to one warp, so four tiles are in work at a time and a
-//     tile takes one pass of the softmax; the warps' outputs are joined in shared memory when
-//     the item ends.  Weights go into the product with V as two bf16 terms (hi + lo, 2^-17):
-//     the second product hides behind HBM, and the output is off by its own rounding alone.
-//   otherwise: a warp owns 16 of 64 rows and reads every tile; weights are rounded to bf16 once
-//     (2^-9 of each, as elsewhere in this library; 64 rows x two terms would no longer hide).
+// Four consumer warps run both products on mma.sync m16n8k16 (the tensor pipe is far from its
+// limit at these row counts, and a tcgen05 tile would be 128 rows):
+//   paged_step_kernel (R <= 16): a tile belongs to one warp, so four tiles are in work at a
+//     time and a tile takes one pass of the softmax.  The products are S^T = K Q^T and
+//     O^T += V^T P^T: keys and dims fill the 16 rows of the instruction and the queries its 8
+//     columns, so up to 8 rows waste nothing (queries as the 16 rows took twice the
+//     instructions).  The warps' outputs are joined in shared memory when the item ends.
+//     Weights go into the product with V as two bf16 terms (hi + lo, 2^-17): the second
+//     product hides behind HBM, and the output is off by its own rounding alone.
+//   paged_few_kernel (R <= 64): a warp owns 16 of 64 rows and reads every tile; weights are
+//     rounded to bf16 once (2^-9 of each, as elsewhere in this library; 64 rows x two terms
+//     would no longer hide).
 // Keys behind the last visible one are not loaded past their page piece; their scores are
 // replaced, and their V rows (which may hold anything) masked in the fragments.
 #include "paged.cuh"
@@ -26,21 +30,32 @@ using namespace sm100;
 using fastmath::fast_exp2;
 
 constexpr int KT = 32;                // keys of a tile
-constexpr int kConsumers = 4;         // warps 0-3; warp 4 produces
+#ifndef FEW_WARPS
+#define FEW_WARPS 4
+#endif
+constexpr int kConsumers = FEW_WARPS; // warps 0-3; warp 4 produces
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kHalf = KT * 128;  // 32 keys x 64 dims
+#ifndef FEW_LEAD
+#define FEW_LEAD 7
+#endif
+constexpr int kLead = FEW_LEAD;
 template <int D> constexpr int kStages = D == 128 ? 10 : 20;
 template <int D> constexpr uint32_t kTileBytes = KT * D * 2;
 template <int D> constexpr uint32_t kStageBytes = 2 * kTileBytes<D>;
 
 template <int D>
-struct __align__(16) Shared {
-  float o[kConsumers][16][D + 4];     // the warps' outputs of an item (SPLIT)
-  float2 ml[kConsumers][16];
+struct __align__(16) Ring {
   uint64_t full[kStages<D>], empty[kStages<D>];
   int abort;
   PlanSmem plan;
+};
+// The warps' outputs of an item, joined when it ends.
+template <int D, int R>
+struct __align__(16) Join {
+  float o[kConsumers][R][D + 4];
+  float2 ml[kConsumers][R];
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -75,98 +90,357 @@ __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
 }
 
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1)
-paged_attn_few_kernel(const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, int box,
-                      const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ o,
-                      float* __restrict__ lse, PagedParts parts, int* err,
-                      const __grid_constant__ PagedAttn a) {
-  constexpr int ROWS = SPLIT ? 16 : 64;
+template <int D>
+__device__ __forceinline__ void ring_fail(Ring<D>& sm, int* err) {
+  set_device_error(err, MSA_DEVERR_TIMEOUT);
+  *(volatile int*)&sm.abort = 1;
+}
+
+// The producer warp: copies every tile of the run, in order.
+template <int D>
+__device__ __forceinline__ void produce(const CUtensorMap& tm_k, const CUtensorMap& tm_v, int box,
+                                        unsigned char* ring, Ring<D>& sm, Run r, int* err,
+                                        const PagedAttn& a) {
   constexpr int ST = kStages<D>;
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* ring = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Shared<D>& sm = *reinterpret_cast<Shared<D>*>(ring + ST * kStageBytes<D>);
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  if (tid == 0) {
-    for (int s = 0; s < ST; ++s) {
+  const int lane = threadIdx.x % 32;
+  const int per = KT / box;                               // page pieces of a tile
+  const int rows = (int)(a.g.n_pages * a.hkv * a.g.page);
+  int64_t step = 0;
+  bool ok = true;
+  do {
+    const int tile0 = run_first(a, r), nt = run_tiles(a, r), vis = tile_keys(a, r.v, r.rt);
+    if (nt == 0) break;                                   // the run ends in the item's lead
+    // row of piece i of the item's part of this run in the pools, `rows` (reads as zeros)
+    // for an entry that is no page, -1 past the last visible key
+    auto piece_row = [&](int i) -> int {
+      const int key = tile0 * KT + i * box;
+      if (i >= nt * per || key >= vis) return -1;
+      const int pg = key_page(a, r.s, key, err);
+      return pg < 0 ? rows : (int)(((int64_t)pg * a.hkv + r.g) * a.g.page + key % (int)a.g.page);
+    };
+    int cur = piece_row(lane), nxt = piece_row(32 + lane);
+    for (int it = 0; it < nt; ++it, ++step) {
+      const int at = it * per;                            // first piece of the tile
+      if (at > 0 && at % 32 == 0) {
+        cur = nxt;
+        nxt = piece_row(at + 32 + lane);
+      }
+      const int st = (int)(step % ST);
+      if (step >= ST && !mbar_wait_warp(&sm.empty[st], (uint32_t)((step / ST) - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      const int y = __shfl_sync(0xffffffffu, cur, (at & 31) + (lane < per ? lane : 0));
+      const bool mine = lane < per && y >= 0;
+      const int n = __popc(__ballot_sync(0xffffffffu, mine));
+      if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], (uint32_t)(n * box * D * 4));
+      __syncwarp();
+      if (mine) {
+        unsigned char* dst = ring + st * kStageBytes<D> + lane * box * 128;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          tma_load_2d(dst + h * kHalf, &tm_k, &sm.full[st], h * 64, y);
+          tma_load_2d(dst + kTileBytes<D> + h * kHalf, &tm_v, &sm.full[st], h * 64, y);
+        }
+      }
+    }
+    if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) ok = false;
+  } while (ok && run_next<KT>(a, r));
+  if (!ok) {
+    if (lane == 0) ring_fail(sm, err);
+    // no copy may still be landing when the CTA ends
+    for (int64_t s = step > ST ? step - ST : 0; s < step; ++s)
+      mbar_wait_warp(&sm.full[s % ST], (uint32_t)(s / ST) & 1);
+  }
+}
+
+// Set-up shared by both kernels: barriers, this CTA's record, the run.
+template <int D>
+__device__ __forceinline__ Run begin(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                     Ring<D>& sm, int readers, const PagedParts& parts,
+                                     const PagedAttn& a) {
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    for (int s = 0; s < kStages<D>; ++s) {
       mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], SPLIT ? 1 : kConsumers);
+      mbar_init(&sm.empty[s], readers);
     }
     sm.abort = 0;
     fence_mbar_init();
     parts.rec[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  Run r = paged_plan<KT, kThreads>(a, &sm.plan);          // synchronises the CTA
-  if (r.left <= 0) return;
-  volatile int* abort_flag = &sm.abort;
-  auto fail = [&]() { set_device_error(err, MSA_DEVERR_TIMEOUT); *abort_flag = 1; };
+  return paged_plan<KT, kThreads>(a, &sm.plan);           // synchronises the CTA
+}
 
+// ------------------------------------------------------------------ up to 8 * NQ rows
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, int box,
+                  const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ o,
+                  float* __restrict__ lse, PagedParts parts, int* err,
+                  const __grid_constant__ PagedAttn a) {
+  constexpr int R = 8 * NQ, ST = kStages<D>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* ring = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ring<D>& sm = *reinterpret_cast<Ring<D>*>(ring + ST * kStageBytes<D>);
+  Join<D, R>& jn = *reinterpret_cast<Join<D, R>*>(ring + ST * kStageBytes<D> + sizeof(Ring<D>));
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  Run r = begin<D>(tm_k, tm_v, sm, 1, parts, a);
+  if (r.at >= r.end) return;
   if (warp == kConsumers) {
-    // ------------------------------------------------------------ producer
-    const int per = KT / box;                             // page pieces of a tile
-    if (lane == 0) {
-      prefetch_tmap(&tm_k);
-      prefetch_tmap(&tm_v);
-    }
-    const int rows = (int)(a.g.n_pages * a.hkv * a.g.page);
-    int64_t step = 0;
-    bool ok = true;
-    do {
-      const int nt = run_tiles(r), vis = tile_keys(a, r.v, r.rt);
-      // row of piece i of the item's part of this run in the pools, `rows` (reads as zeros)
-      // for an entry that is no page, -1 past the last visible key
-      auto piece_row = [&](int i) -> int {
-        const int key = r.tile * KT + i * box;
-        if (i >= nt * per || key >= vis) return -1;
-        const int pg = key_page(a, r.s, key, err);
-        return pg < 0 ? rows : (int)(((int64_t)pg * a.hkv + r.g) * a.g.page + key % (int)a.g.page);
-      };
-      int cur = piece_row(lane), nxt = piece_row(32 + lane);
-      for (int it = 0; it < nt; ++it, ++step) {
-        const int at = it * per;                          // first piece of the tile
-        if (at > 0 && at % 32 == 0) {
-          cur = nxt;
-          nxt = piece_row(at + 32 + lane);
-        }
-        const int st = (int)(step % ST);
-        if (step >= ST && !mbar_wait_warp(&sm.empty[st], (uint32_t)((step / ST) - 1) & 1)) {
-          ok = false;
-          break;
-        }
-        const int y = __shfl_sync(0xffffffffu, cur, (at & 31) + (lane < per ? lane : 0));
-        const bool mine = lane < per && y >= 0;
-        const int n = __popc(__ballot_sync(0xffffffffu, mine));
-        if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], (uint32_t)(n * box * D * 4));
-        __syncwarp();
-        if (mine) {
-          unsigned char* dst = ring + st * kStageBytes<D> + lane * box * 128;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            tma_load_2d(dst + h * kHalf, &tm_k, &sm.full[st], h * 64, y);
-            tma_load_2d(dst + kTileBytes<D> + h * kHalf, &tm_v, &sm.full[st], h * 64, y);
-          }
-        }
-      }
-      if (__any_sync(0xffffffffu, *abort_flag != 0)) ok = false;
-    } while (ok && run_next<KT>(a, r));
-    if (!ok) {
-      if (lane == 0) fail();
-      // no copy may still be landing when the CTA ends
-      for (int64_t s = step > ST ? step - ST : 0; s < step; ++s)
-        mbar_wait_warp(&sm.full[s % ST], (uint32_t)(s / ST) & 1);
-    }
+    produce<D>(tm_k, tm_v, box, ring, sm, r, err, a);
     return;
   }
-
-  // ------------------------------------------------------------ consumers
+  // thread (gr, t4) of a warp: scores of keys gr, gr + 8 of a 16-key block and queries 2 t4,
+  // 2 t4 + 1 of each 8; outputs of dims gr, gr + 8 of a 16-dim block and the same queries
   const int gr = lane >> 2, t4 = lane & 3, mi = lane >> 3, ri = lane & 7;
-  const int row0 = SPLIT ? gr : warp * 16 + gr;           // this thread's rows: row0, row0 + 8
+  // ldmatrix rows: K block (keys (mi & 1) * 8 + ri, dims chunk mi >> 1), V block (keys
+  // (mi >> 1) * 8 + ri, dims chunk mi & 1); chunk c of row r sits at c ^ (r % 8)
+  const uint32_t k_row = (uint32_t)((mi & 1) * 8 + ri) * 128u;
+  const uint32_t v_row = (uint32_t)((mi >> 1) * 8 + ri) * 128u;
+  uint32_t k_off[4], v_off[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    k_off[j] = k_row + (uint32_t)((2 * j + (mi >> 1)) ^ ri) * 16u;
+    v_off[j] = v_row + (uint32_t)((2 * j + (mi & 1)) ^ ri) * 16u;
+  }
   int64_t step = 0;
   bool first_item = true, aborted = false;
   do {
-    const int nt = run_tiles(r), vis = tile_keys(a, r.v, r.rt);
+    const int tile0 = run_first(a, r), nt = run_tiles(a, r), vis = tile_keys(a, r.v, r.rt);
+    if (nt == 0) break;                                   // the run ends in the item's lead
+    uint32_t qb[NQ][D / 16][2];
+    int see[NQ][2];                                       // keys of queries 2 t4, 2 t4 + 1
+    int least = INT32_MAX;                                // of any query of this thread
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int row = n * 8 + gr, t_in = r.rt * a.tt + row / a.G;
+      const bool on = row < a.tt * a.G && t_in < r.v.n;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          q + (r.v.tok0 + t_in) * a.qs + (int64_t)(r.g * a.G + row % a.G) * D);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        qb[n][ks][0] = on ? __ldg(src + ks * 8 + t4) : 0u;
+        qb[n][ks][1] = on ? __ldg(src + ks * 8 + 4 + t4) : 0u;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = n * 8 + 2 * t4 + e, c_in = r.rt * a.tt + c / a.G;
+        const bool there = c < a.tt * a.G && c_in < r.v.n;
+        see[n][e] =
+            there ? (int)max(0LL, min((long long)r.v.past + c_in + 1, (long long)r.v.cap)) : 0;
+        if (there) least = min(least, see[n][e]);
+      }
+    }
+    // (queries that are not there need no mask: their results go nowhere)
+    least = __reduce_min_sync(0xffffffffu, least);
+    float m[NQ][2], l[NQ][2], acc[NQ][D / 16][4];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      m[n][0] = m[n][1] = -CUDART_INF_F;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][dt][e] = 0.f;
+    }
+    for (int it = 0; it < nt; ++it, ++step) {
+      if ((int)(step % kConsumers) != warp) continue;
+      const int st = (int)(step % ST);
+      if (aborted || __any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) {
+        aborted = true;
+        continue;
+      }
+      if (!mbar_wait_warp(&sm.full[st], (uint32_t)(step / ST) & 1)) {
+        if (lane == 0) ring_fail(sm, err);
+        aborted = true;
+        continue;
+      }
+      const uint32_t sk = smem_u32(ring + st * kStageBytes<D>), sv = sk + kTileBytes<D>;
+      const int key0 = (tile0 + it) * KT;
+      float s[NQ][2][4];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][kb][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          uint32_t f[4];
+          ldsm4(sk + k_off[ks & 3] + (ks >> 2) * kHalf + kb * 2048, f);
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) mma16816(s[n][kb], f, qb[n][ks][0], qb[n][ks][1]);
+        }
+      // online softmax over the tile's keys: s[.][kb][e] is key kb * 16 + gr + 8 (e / 2) and
+      // query 2 t4 + e % 2
+      const bool inside = key0 + KT <= least;
+      bool moved = false;
+      uint32_t ph[NQ][4], pl[NQ][4];                      // 8-key blocks of P^T, bf16 pairs
+      float alpha[NQ][2];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        float mx[2] = {-CUDART_INF_F, -CUDART_INF_F}, add[2] = {0.f, 0.f}, ref[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = s[n][kb][e] * a.scale_log2;
+            if (!inside && key0 + kb * 16 + gr + 8 * (e >> 1) >= see[n][e & 1]) x = -CUDART_INF_F;
+            s[n][kb][e] = x;
+            mx[e & 1] = fmaxf(mx[e & 1], x);
+          }
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) {
+          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], w));
+          mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], w));
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mn = fmaxf(m[n][e], mx[e]);
+          ref[e] = mn == -CUDART_INF_F ? 0.f : mn;
+          alpha[n][e] = fast_exp2(m[n][e] - ref[e]);
+          moved |= alpha[n][e] != 1.f;
+          m[n][e] = mn;
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float p0 = fast_exp2(s[n][kb][2 * h] - ref[0]);
+            const float p1 = fast_exp2(s[n][kb][2 * h + 1] - ref[1]);
+            add[0] += p0;
+            add[1] += p1;
+            const uint32_t hi = pack_bf16x2(p0, p1);
+            ph[n][2 * kb + h] = transpose8(hi);
+            pl[n][2 * kb + h] =
+                transpose8(pack_bf16x2(p0 - bf16lo_to_f32(hi), p1 - bf16hi_to_f32(hi)));
+          }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l[n][e] = l[n][e] * alpha[n][e] + add[e];
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][dt][e] *= alpha[n][e & 1];
+      }
+      const int lim = vis - key0;                         // keys of the tile that exist
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) {
+          uint32_t f[4];                                  // (dims, keys): (0,0) (8,0) (0,8) (8,8)
+          ldsm4_t(sv + v_off[dt & 3] + (dt >> 2) * kHalf + kb * 2048, f);
+          if (lim < KT) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) f[w] = keep_keys(f[w], kb * 16 + (w >> 1) * 8 + 2 * t4, lim);
+          }
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            mma16816(acc[n][dt], f, ph[n][2 * kb], ph[n][2 * kb + 1]);
+            mma16816(acc[n][dt], f, pl[n][2 * kb], pl[n][2 * kb + 1]);
+          }
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[st]);
+    }
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
+        const int row = n * 8 + 2 * t4 + e;
+        if (gr == 0) jn.ml[warp][row] = make_float2(m[n][e], l[n][e]);
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) {
+          jn.o[warp][row][dt * 16 + gr] = acc[n][dt][e];
+          jn.o[warp][row][dt * 16 + gr + 8] = acc[n][dt][2 + e];
+        }
+      }
+    consumers_sync();
+    // join the four warps: R rows x D columns over 128 threads, four columns at a time
+    const bool whole = nt == r.tiles;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (first_item ? 0 : 1);
+#pragma unroll
+    for (int i = tid; i < R * D / 4; i += kConsumers * 32) {
+      const int row = i / (D / 4), c = i % (D / 4) * 4, t_in = r.rt * a.tt + row / a.G;
+      if (row >= a.tt * a.G || t_in >= r.v.n) continue;
+      float mx = -CUDART_INF_F, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) mx = fmaxf(mx, jn.ml[w][row].x);
+      const float base = mx == -CUDART_INF_F ? 0.f : mx;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) {
+        const float f = fast_exp2(jn.ml[w][row].x - base);
+        sum = fmaf(jn.ml[w][row].y, f, sum);
+        const float4 x = *reinterpret_cast<const float4*>(&jn.o[w][row][c]);
+        y.x = fmaf(x.x, f, y.x);
+        y.y = fmaf(x.y, f, y.y);
+        y.z = fmaf(x.z, f, y.z);
+        y.w = fmaf(x.w, f, y.w);
+      }
+      const int64_t qrow = (r.v.tok0 + t_in) * a.hq + r.g * a.G + row % a.G;
+      if (whole) {
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        *reinterpret_cast<uint2*>(o + qrow * D + c) =
+            make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+        if (c == 0 && lse != nullptr)
+          lse[qrow] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -CUDART_INF_F;
+      } else {
+        *reinterpret_cast<float4*>(parts.o + (slot * R + row) * D + c) = y;
+        if (c == 0) parts.ml[slot * R + row] = make_float2(mx, sum);
+      }
+    }
+    if (!whole && tile0 == 0 && tid == 0)
+      parts.rec[blockIdx.x] = item_record(a, r, first_item);
+    consumers_sync();
+    first_item = false;
+  } while (run_next<KT>(a, r));
+}
+
+// ------------------------------------------------------------------ up to 64 rows
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_few_kernel(const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, int box,
+                 const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ o,
+                 float* __restrict__ lse, PagedParts parts, int* err,
+                 const __grid_constant__ PagedAttn a) {
+  constexpr int R = 64, ST = kStages<D>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* ring = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ring<D>& sm = *reinterpret_cast<Ring<D>*>(ring + ST * kStageBytes<D>);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  Run r = begin<D>(tm_k, tm_v, sm, kConsumers, parts, a);
+  if (r.at >= r.end) return;
+  if (warp == kConsumers) {
+    produce<D>(tm_k, tm_v, box, ring, sm, r, err, a);
+    return;
+  }
+  const int gr = lane >> 2, t4 = lane & 3, mi = lane >> 3, ri = lane & 7;
+  const int row0 = warp * 16 + gr;           // this thread's rows: row0, row0 + 8
+  int64_t step = 0;
+  bool first_item = true, aborted = false;
+  do {
+    const int tile0 = run_first(a, r), nt = run_tiles(a, r), vis = tile_keys(a, r.v, r.rt);
+    if (nt == 0) break;                                   // the run ends in the item's lead
     int see[2];
     bool there[2];                                        // rows that hold a query
     uint32_t qa[D / 16][4];
@@ -192,16 +466,15 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap tm_k,
       for (int e = 0; e < 4; ++e) acc[dt][e] = 0.f;
 
     for (int it = 0; it < nt; ++it, ++step) {
-      if (SPLIT && (int)(step % kConsumers) != warp) continue;
       const int st = (int)(step % ST);
-      if (aborted || __any_sync(0xffffffffu, *abort_flag != 0)) { aborted = true; continue; }
+      if (aborted || __any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) { aborted = true; continue; }
       if (!mbar_wait_warp(&sm.full[st], (uint32_t)(step / ST) & 1)) {
-        if (lane == 0) fail();
+        if (lane == 0) ring_fail(sm, err);
         aborted = true;
         continue;
       }
       const uint32_t sk = smem_u32(ring + st * kStageBytes<D>), sv = sk + kTileBytes<D>;
-      const int key0 = (r.tile + it) * KT;
+      const int key0 = (tile0 + it) * KT;
       float s[KT / 8][4];
 #pragma unroll
       for (int nt8 = 0; nt8 < KT / 8; ++nt8)
@@ -262,14 +535,12 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int lim = vis - key0;                         // keys of the tile that exist
 #pragma unroll
       for (int kk = 0; kk < KT / 16; ++kk) {
-        uint32_t ph[4], pl[4];
+        uint32_t ph[4];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {                     // (row, key half): (0,0) (1,0) (0,1) (1,1)
           const float p0 = s[2 * kk + (w >> 1)][2 * (w & 1)];
           const float p1 = s[2 * kk + (w >> 1)][2 * (w & 1) + 1];
           ph[w] = pack_bf16x2(p0, p1);
-          if (SPLIT)
-            pl[w] = pack_bf16x2(p0 - bf16lo_to_f32(ph[w]), p1 - bf16hi_to_f32(ph[w]));
         }
 #pragma unroll
         for (int dt = 0; dt < D / 8; dt += 2) {
@@ -281,10 +552,6 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap tm_k,
           }
           mma16816(acc[dt], ph, b[0], b[1]);
           mma16816(acc[dt + 1], ph, b[2], b[3]);
-          if (SPLIT) {
-            mma16816(acc[dt], pl, b[0], b[1]);
-            mma16816(acc[dt + 1], pl, b[2], b[3]);
-          }
         }
       }
       __syncwarp();
@@ -295,119 +562,77 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap tm_k,
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
     }
-    const bool whole = r.tile == 0 && nt == r.tiles;
+    const bool whole = nt == r.tiles;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (first_item ? 0 : 1);
-    if (SPLIT) {
-      // join the four warps: thread = (row tid / 8, D / 8 columns)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (t4 == 0) sm.ml[warp][gr + 8 * i] = make_float2(m[i], l[i]);
-#pragma unroll
-        for (int dt = 0; dt < D / 8; ++dt)
-          *reinterpret_cast<float2*>(&sm.o[warp][gr + 8 * i][dt * 8 + 2 * t4]) =
-              make_float2(acc[dt][2 * i], acc[dt][2 * i + 1]);
-      }
-      consumers_sync();
-      const int row = tid / 8, c0 = (tid % 8) * 4, t_in = r.rt * a.tt + row / a.G;
-      const bool on = row < a.tt * a.G && t_in < r.v.n;
-      float mx = -CUDART_INF_F, sum = 0.f, w[kConsumers];
-#pragma unroll
-      for (int i = 0; i < kConsumers; ++i) mx = fmaxf(mx, sm.ml[i][row].x);
-      const float base = mx == -CUDART_INF_F ? 0.f : mx;
-#pragma unroll
-      for (int i = 0; i < kConsumers; ++i) {
-        w[i] = fast_exp2(sm.ml[i][row].x - base);
-        sum = fmaf(sm.ml[i][row].y, w[i], sum);
-      }
-      const float inv = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+    for (int i = 0; i < 2; ++i) {
+      const int row = row0 + 8 * i, t_in = r.rt * a.tt + row / a.G;
+      if (row >= a.tt * a.G || t_in >= r.v.n) continue;
       const int64_t qrow = (r.v.tok0 + t_in) * a.hq + r.g * a.G + row % a.G;
+      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        const int c = j * 32 + c0;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kConsumers; ++i) {
-          const float4 x = *reinterpret_cast<const float4*>(&sm.o[i][row][c]);
-          y.x = fmaf(x.x, w[i], y.x);
-          y.y = fmaf(x.y, w[i], y.y);
-          y.z = fmaf(x.z, w[i], y.z);
-          y.w = fmaf(x.w, w[i], y.w);
-        }
-        if (!on) continue;
-        if (whole) {
-          *reinterpret_cast<uint2*>(o + qrow * D + c) =
-              make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-        } else {
-          *reinterpret_cast<float4*>(parts.o + (slot * ROWS + row) * D + c) = y;
-        }
+      for (int dt = 0; dt < D / 8; ++dt) {
+        const float x = acc[dt][2 * i], y = acc[dt][2 * i + 1];
+        const int c = dt * 8 + 2 * t4;
+        if (whole)
+          *reinterpret_cast<uint32_t*>(o + qrow * D + c) = pack_bf16x2(x * inv, y * inv);
+        else
+          *reinterpret_cast<float2*>(parts.o + (slot * R + row) * D + c) = make_float2(x, y);
       }
-      if (on && tid % 8 == 0) {
-        if (!whole) parts.ml[slot * ROWS + row] = make_float2(mx, sum);
-        else if (lse != nullptr) lse[qrow] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -CUDART_INF_F;
-      }
-      consumers_sync();
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = row0 + 8 * i, t_in = r.rt * a.tt + row / a.G;
-        if (row >= a.tt * a.G || t_in >= r.v.n) continue;
-        const int64_t qrow = (r.v.tok0 + t_in) * a.hq + r.g * a.G + row % a.G;
-        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
-#pragma unroll
-        for (int dt = 0; dt < D / 8; ++dt) {
-          const float x = acc[dt][2 * i], y = acc[dt][2 * i + 1];
-          const int c = dt * 8 + 2 * t4;
-          if (whole)
-            *reinterpret_cast<uint32_t*>(o + qrow * D + c) = pack_bf16x2(x * inv, y * inv);
-          else
-            *reinterpret_cast<float2*>(parts.o + (slot * ROWS + row) * D + c) = make_float2(x, y);
-        }
-        if (t4 == 0) {
-          if (!whole) parts.ml[slot * ROWS + row] = make_float2(m[i], l[i]);
-          else if (lse != nullptr)
-            lse[qrow] = l[i] > 0.f ? (m[i] + log2f(l[i])) * kLn2 : -CUDART_INF_F;
-        }
+      if (t4 == 0) {
+        if (!whole) parts.ml[slot * R + row] = make_float2(m[i], l[i]);
+        else if (lse != nullptr)
+          lse[qrow] = l[i] > 0.f ? (m[i] + log2f(l[i])) * kLn2 : -CUDART_INF_F;
       }
     }
-    if (!whole && r.tile == 0 && tid == 0)
-      parts.rec[blockIdx.x] = make_int4(r.s, r.g, r.rt | (first_item ? 0 : 1 << 30),
-                                        item_parts(r.share - r.left, r.tiles, r.share));
+    if (!whole && tile0 == 0 && tid == 0)
+      parts.rec[blockIdx.x] = item_record(a, r, first_item);
     first_item = false;
   } while (run_next<KT>(a, r));
 }
 
-template <int D, bool SPLIT>
-cudaError_t run(PagedAttn& a, const HeadShape& s, const void* q, const void* kp, const void* vp,
-                void* o, float* lse, const PagedParts& parts, int* err, cudaStream_t st) {
-  constexpr int ROWS = SPLIT ? 16 : 64;
-  a.tt = ROWS / a.G;
+template <typename K>
+cudaError_t run(K kernel, int rows, size_t smem, PagedAttn& a, const HeadShape& s, const void* q,
+                const void* kp, const void* vp, void* o, float* lse, const PagedParts& parts,
+                int* err, cudaStream_t st) {
+  a.tt = rows / a.G;
+  a.lead = kLead;
   const int box = a.g.page % 32 == 0 ? 32 : 16;           // keys of one copy: they share a page
-  const int64_t rows = a.g.n_pages * a.hkv * a.g.page;
+  const int64_t pool = a.g.n_pages * a.hkv * a.g.page;
   CUtensorMap mk{}, mv{};
-  if (rows > 0 && (!make_bf16_2d_map(&mk, kp, rows, D, box) ||
-                   !make_bf16_2d_map(&mv, vp, rows, D, box)))
+  if (!make_bf16_2d_map(&mk, kp, pool, s.d, box) || !make_bf16_2d_map(&mv, vp, pool, s.d, box))
     return cudaErrorInvalidValue;
-  const size_t smem = 1024 + kStages<D> * kStageBytes<D> + sizeof(Shared<D>);
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_few_kernel<D, SPLIT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int grid = paged_grid();
-  paged_attn_few_kernel<D, SPLIT><<<grid, kThreads, smem, st>>>(
-      mk, mv, box, (const __nv_bfloat16*)q, (__nv_bfloat16*)o, lse, parts, err, a);
+  kernel<<<grid, kThreads, smem, st>>>(mk, mv, box, (const __nv_bfloat16*)q, (__nv_bfloat16*)o,
+                                       lse, parts, err, a);
   e = cudaGetLastError();
-  return e == cudaSuccess ? launch_paged_combine(s, a, grid, ROWS, parts, o, lse, st) : e;
+  return e == cudaSuccess ? launch_paged_combine(s, a, grid, rows, parts, o, lse, st) : e;
+}
+
+template <int D>
+cudaError_t run_rows(int rows, PagedAttn& a, const HeadShape& s, const void* q, const void* kp,
+                     const void* vp, void* o, float* lse, const PagedParts& parts, int* err,
+                     cudaStream_t st) {
+  const size_t ring = 1024 + kStages<D> * kStageBytes<D> + sizeof(Ring<D>);
+  if (rows <= 8)
+    return run(paged_step_kernel<D, 1>, 8, ring + sizeof(Join<D, 8>), a, s, q, kp, vp, o, lse,
+               parts, err, st);
+  if (rows <= 16)
+    return run(paged_step_kernel<D, 2>, 16, ring + sizeof(Join<D, 16>), a, s, q, kp, vp, o, lse,
+               parts, err, st);
+  return run(paged_few_kernel<D>, 64, ring, a, s, q, kp, vp, o, lse, parts, err, st);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_few(const HeadShape& s, PagedAttn a, bool split, const void* q,
+cudaError_t launch_paged_few(const HeadShape& s, PagedAttn a, int rows, const void* q,
                              const void* kp, const void* vp, void* o, float* lse,
                              const PagedParts& parts, int* err, cudaStream_t st) {
-  if (s.d == 128)
-    return split ? run<128, true>(a, s, q, kp, vp, o, lse, parts, err, st)
-                 : run<128, false>(a, s, q, kp, vp, o, lse, parts, err, st);
-  return split ? run<64, true>(a, s, q, kp, vp, o, lse, parts, err, st)
-               : run<64, false>(a, s, q, kp, vp, o, lse, parts, err, st);
+  return s.d == 128 ? run_rows<128>(rows, a, s, q, kp, vp, o, lse, parts, err, st)
+                    : run_rows<64>(rows, a, s, q, kp, vp, o, lse, parts, err, st);
 }
 
 }  // namespace msa

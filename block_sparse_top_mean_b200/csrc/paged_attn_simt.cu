@@ -34,9 +34,11 @@ paged_attn_simt_kernel(const T* __restrict__ q, const T* __restrict__ kp,
   const int tid = threadIdx.x, row = tid / kLanes, l8 = tid % kLanes;
   Run r = paged_plan<KT, THREADS>(a, &sm.plan);
   if (tid == 0) parts.rec[blockIdx.x] = make_int4(0, 0, 0, 0);
-  if (r.left <= 0) return;
+  if (r.at >= r.end) return;
   bool first_item = true;
   do {
+    const int tile0 = run_first(a, r), nt = run_tiles(a, r);
+    if (nt == 0) break;                                   // the run ends in the item's lead
     const int t_in = r.rt * a.tt + row / a.G, h = row % a.G;
     const bool on = row < a.tt * a.G && t_in < r.v.n;
     const int64_t tok = r.v.tok0 + t_in;
@@ -58,9 +60,8 @@ paged_attn_simt_kernel(const T* __restrict__ q, const T* __restrict__ kp,
     float acc[D / kLanes];
 #pragma unroll
     for (int i = 0; i < D / kLanes; ++i) acc[i] = 0.f;
-    const int nt = run_tiles(r);
     for (int it = 0; it < nt; ++it) {
-      const int key0 = (r.tile + it) * KT;
+      const int key0 = (tile0 + it) * KT;
       __syncthreads();
       for (int i = tid; i < 2 * KT * CH; i += THREADS) {
         const int which = i / (KT * CH), j = i % (KT * CH), kr = j / CH, c = j % CH;
@@ -125,7 +126,7 @@ paged_attn_simt_kernel(const T* __restrict__ q, const T* __restrict__ kp,
       }
       __syncwarp();
     }
-    const bool whole = r.tile == 0 && nt == r.tiles;
+    const bool whole = nt == r.tiles;
     if (whole) {
       if (on) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -142,9 +143,8 @@ paged_attn_simt_kernel(const T* __restrict__ q, const T* __restrict__ kp,
       for (int i = 0; i < D / kLanes; i += 4)
         *reinterpret_cast<float4*>(&parts.o[(slot * ROWS + row) * D + ((i / 4) * kLanes + l8) * 4]) =
             make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-      if (tid == 0 && r.tile == 0)
-        parts.rec[blockIdx.x] = make_int4(r.s, r.g, r.rt | (first_item ? 0 : 1 << 30),
-                                          item_parts(r.share - r.left, r.tiles, r.share));
+      if (tid == 0 && tile0 == 0)
+        parts.rec[blockIdx.x] = item_record(a, r, first_item);
     }
     first_item = false;
   } while (run_next<KT>(a, r));
@@ -154,6 +154,7 @@ template <typename T, int D, int ROWS>
 cudaError_t run(PagedAttn& a, const HeadShape& s, const void* q, const void* kp, const void* vp,
                 void* o, float* lse, const PagedParts& parts, int* err, cudaStream_t st) {
   a.tt = ROWS / a.G;
+  a.lead = 1;
   const size_t smem = sizeof(Smem<D, ROWS>);
   cudaError_t e = cudaFuncSetAttribute(paged_attn_simt_kernel<T, D, ROWS>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
