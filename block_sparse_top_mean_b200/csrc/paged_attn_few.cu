@@ -41,13 +41,19 @@ constexpr uint32_t kHalf = KT * 128;  // 32 keys x 64 dims
 #define FEW_LEAD 7
 #endif
 constexpr int kLead = FEW_LEAD;
-template <int D> constexpr int kStages = D == 128 ? 10 : 20;
+#ifndef FEW_ST
+#define FEW_ST 12
+#endif
 template <int D> constexpr uint32_t kTileBytes = KT * D * 2;
 template <int D> constexpr uint32_t kStageBytes = 2 * kTileBytes<D>;
 
-template <int D>
+// ST stages.  Where a tile belongs to one warp, ST is a multiple of the warps, so that a stage
+// always belongs to the same warp: a parity wait tells a phase only from its neighbours, and a
+// warp that took over another's stage could be a whole round ahead of a copy that is late.
+template <int D, int ST>
 struct __align__(16) Ring {
-  uint64_t full[kStages<D>], empty[kStages<D>];
+  static_assert(ST % kConsumers == 0, "a stage keeps its warp");
+  uint64_t full[ST], empty[ST];
   int abort;
   PlanSmem plan;
 };
@@ -90,22 +96,36 @@ __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
 }
 
-template <int D>
-__device__ __forceinline__ void ring_fail(Ring<D>& sm, int* err) {
+template <int D, int ST>
+__device__ __forceinline__ void ring_fail(Ring<D, ST>& sm, int* err) {
   set_device_error(err, MSA_DEVERR_TIMEOUT);
   *(volatile int*)&sm.abort = 1;
 }
 
+// Waits for a phase of one of the ring's barriers, for the whole warp; false when the wait ran
+// out (after ~2 s) or another warp's did.
+template <int D, int ST>
+__device__ __forceinline__ bool ring_wait(Ring<D, ST>& sm, uint64_t* bar, uint32_t parity, int* err) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  const long long t0 = clock64();
+  while (!ok && *(volatile int*)&sm.abort == 0 && clock64() - t0 < 4000000000LL)
+    ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if (threadIdx.x % 32 == 0) ring_fail(sm, err);
+  return false;
+}
+
 // The producer warp: copies every tile of the run, in order.
-template <int D>
+template <int D, int ST>
 __device__ __forceinline__ void produce(const CUtensorMap& tm_k, const CUtensorMap& tm_v, int box,
-                                        unsigned char* ring, Ring<D>& sm, Run r, int* err,
+                                        unsigned char* ring, Ring<D, ST>& sm, Run r, int* err,
                                         const PagedAttn& a) {
-  constexpr int ST = kStages<D>;
   const int lane = threadIdx.x % 32;
   const int per = KT / box;                               // page pieces of a tile
   const int rows = (int)(a.g.n_pages * a.hkv * a.g.page);
-  int64_t step = 0;
+  int step = 0, st = 0;                                   // copies so far; the next one's stage
+  uint32_t ph = 1;                                        // of the stage's empty barrier
   bool ok = true;
   do {
     const int tile0 = run_first(a, r), nt = run_tiles(a, r), vis = tile_keys(a, r.v, r.rt);
@@ -125,8 +145,8 @@ __device__ __forceinline__ void produce(const CUtensorMap& tm_k, const CUtensorM
         cur = nxt;
         nxt = piece_row(at + 32 + lane);
       }
-      const int st = (int)(step % ST);
-      if (step >= ST && !mbar_wait_warp(&sm.empty[st], (uint32_t)((step / ST) - 1) & 1)) {
+      // (the first pass over the ring waits for the phase before the first: it is over)
+      if (!ring_wait(sm, &sm.empty[st], ph, err)) {
         ok = false;
         break;
       }
@@ -143,26 +163,26 @@ __device__ __forceinline__ void produce(const CUtensorMap& tm_k, const CUtensorM
           tma_load_2d(dst + kTileBytes<D> + h * kHalf, &tm_v, &sm.full[st], h * 64, y);
         }
       }
+      if (++st == ST) {
+        st = 0;
+        ph ^= 1;
+      }
     }
-    if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) ok = false;
   } while (ok && run_next<KT>(a, r));
-  if (!ok) {
-    if (lane == 0) ring_fail(sm, err);
-    // no copy may still be landing when the CTA ends
-    for (int64_t s = step > ST ? step - ST : 0; s < step; ++s)
+  if (!ok)                                                // no copy may land after the CTA ends
+    for (int s = step > ST ? step - ST : 0; s < step; ++s)
       mbar_wait_warp(&sm.full[s % ST], (uint32_t)(s / ST) & 1);
-  }
 }
 
 // Set-up shared by both kernels: barriers, this CTA's record, the run.
-template <int D>
+template <int D, int ST>
 __device__ __forceinline__ Run begin(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                     Ring<D>& sm, int readers, const PagedParts& parts,
+                                     Ring<D, ST>& sm, int readers, const PagedParts& parts,
                                      const PagedAttn& a) {
   if (threadIdx.x == 0) {
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
-    for (int s = 0; s < kStages<D>; ++s) {
+    for (int s = 0; s < ST; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], readers);
     }
@@ -180,24 +200,24 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-template <int D, int NQ>
+template <int D, int NQ, int ST>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, int box,
                   const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ o,
                   float* __restrict__ lse, PagedParts parts, int* err,
                   const __grid_constant__ PagedAttn a) {
-  constexpr int R = 8 * NQ, ST = kStages<D>;
+  constexpr int R = 8 * NQ;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* ring = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Ring<D>& sm = *reinterpret_cast<Ring<D>*>(ring + ST * kStageBytes<D>);
-  Join<D, R>& jn = *reinterpret_cast<Join<D, R>*>(ring + ST * kStageBytes<D> + sizeof(Ring<D>));
+  Ring<D, ST>& sm = *reinterpret_cast<Ring<D, ST>*>(ring + ST * kStageBytes<D>);
+  Join<D, R>& jn = *reinterpret_cast<Join<D, R>*>(ring + ST * kStageBytes<D> + sizeof(Ring<D, ST>));
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  Run r = begin<D>(tm_k, tm_v, sm, 1, parts, a);
+  Run r = begin(tm_k, tm_v, sm, 1, parts, a);
   if (r.at >= r.end) return;
   if (warp == kConsumers) {
-    produce<D>(tm_k, tm_v, box, ring, sm, r, err, a);
+    produce(tm_k, tm_v, box, ring, sm, r, err, a);
     return;
   }
   // thread (gr, t4) of a warp: scores of keys gr, gr + 8 of a 16-key block and queries 2 t4,
@@ -213,7 +233,8 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
     k_off[j] = k_row + (uint32_t)((2 * j + (mi >> 1)) ^ ri) * 16u;
     v_off[j] = v_row + (uint32_t)((2 * j + (mi & 1)) ^ ri) * 16u;
   }
-  int64_t step = 0;
+  int turn = warp, st = warp;                             // tiles until this warp's; its stage
+  uint32_t phase = 0;
   bool first_item = true, aborted = false;
   do {
     const int tile0 = run_first(a, r), nt = run_tiles(a, r), vis = tile_keys(a, r.v, r.rt);
@@ -253,17 +274,11 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[n][dt][e] = 0.f;
     }
-    for (int it = 0; it < nt; ++it, ++step) {
-      if ((int)(step % kConsumers) != warp) continue;
-      const int st = (int)(step % ST);
-      if (aborted || __any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) {
+    int it = turn;
+    for (; it < nt; it += kConsumers) {
+      if (aborted || !ring_wait(sm, &sm.full[st], phase, err)) {
         aborted = true;
-        continue;
-      }
-      if (!mbar_wait_warp(&sm.full[st], (uint32_t)(step / ST) & 1)) {
-        if (lane == 0) ring_fail(sm, err);
-        aborted = true;
-        continue;
+        break;
       }
       const uint32_t sk = smem_u32(ring + st * kStageBytes<D>), sv = sk + kTileBytes<D>;
       const int key0 = (tile0 + it) * KT;
@@ -357,7 +372,12 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[st]);
+      if ((st += kConsumers) >= ST) {
+        st -= ST;
+        phase ^= 1;
+      }
     }
+    turn = it - nt;
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -415,28 +435,29 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
 }
 
 // ------------------------------------------------------------------ up to 64 rows
-template <int D>
+template <int D, int ST>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_few_kernel(const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, int box,
                  const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ o,
                  float* __restrict__ lse, PagedParts parts, int* err,
                  const __grid_constant__ PagedAttn a) {
-  constexpr int R = 64, ST = kStages<D>;
+  constexpr int R = 64;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* ring = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Ring<D>& sm = *reinterpret_cast<Ring<D>*>(ring + ST * kStageBytes<D>);
+  Ring<D, ST>& sm = *reinterpret_cast<Ring<D, ST>*>(ring + ST * kStageBytes<D>);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  Run r = begin<D>(tm_k, tm_v, sm, kConsumers, parts, a);
+  Run r = begin(tm_k, tm_v, sm, kConsumers, parts, a);
   if (r.at >= r.end) return;
   if (warp == kConsumers) {
-    produce<D>(tm_k, tm_v, box, ring, sm, r, err, a);
+    produce(tm_k, tm_v, box, ring, sm, r, err, a);
     return;
   }
   const int gr = lane >> 2, t4 = lane & 3, mi = lane >> 3, ri = lane & 7;
   const int row0 = warp * 16 + gr;           // this thread's rows: row0, row0 + 8
-  int64_t step = 0;
+  int st = 0;
+  uint32_t phase = 0;
   bool first_item = true, aborted = false;
   do {
     const int tile0 = run_first(a, r), nt = run_tiles(a, r), vis = tile_keys(a, r.v, r.rt);
@@ -465,13 +486,10 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[dt][e] = 0.f;
 
-    for (int it = 0; it < nt; ++it, ++step) {
-      const int st = (int)(step % ST);
-      if (aborted || __any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) { aborted = true; continue; }
-      if (!mbar_wait_warp(&sm.full[st], (uint32_t)(step / ST) & 1)) {
-        if (lane == 0) ring_fail(sm, err);
+    for (int it = 0; it < nt; ++it) {
+      if (aborted || !ring_wait(sm, &sm.full[st], phase, err)) {
         aborted = true;
-        continue;
+        break;
       }
       const uint32_t sk = smem_u32(ring + st * kStageBytes<D>), sv = sk + kTileBytes<D>;
       const int key0 = (tile0 + it) * KT;
@@ -556,6 +574,10 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[st]);
+      if (++st == ST) {
+        st = 0;
+        phase ^= 1;
+      }
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -591,6 +613,9 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k,
   } while (run_next<KT>(a, r));
 }
 
+template <int D, int ST>
+constexpr size_t ring_bytes() { return 1024 + ST * kStageBytes<D> + sizeof(Ring<D, ST>); }
+
 template <typename K>
 cudaError_t run(K kernel, int rows, size_t smem, PagedAttn& a, const HeadShape& s, const void* q,
                 const void* kp, const void* vp, void* o, float* lse, const PagedParts& parts,
@@ -616,14 +641,17 @@ template <int D>
 cudaError_t run_rows(int rows, PagedAttn& a, const HeadShape& s, const void* q, const void* kp,
                      const void* vp, void* o, float* lse, const PagedParts& parts, int* err,
                      cudaStream_t st) {
-  const size_t ring = 1024 + kStages<D> * kStageBytes<D> + sizeof(Ring<D>);
+  constexpr int ST = FEW_ST * 128 / D;                    // 192 KB of tiles
   if (rows <= 8)
-    return run(paged_step_kernel<D, 1>, 8, ring + sizeof(Join<D, 8>), a, s, q, kp, vp, o, lse,
-               parts, err, st);
-  if (rows <= 16)
-    return run(paged_step_kernel<D, 2>, 16, ring + sizeof(Join<D, 16>), a, s, q, kp, vp, o, lse,
-               parts, err, st);
-  return run(paged_few_kernel<D>, 64, ring, a, s, q, kp, vp, o, lse, parts, err, st);
+    return run(paged_step_kernel<D, 1, ST>, 8, ring_bytes<D, ST>() + sizeof(Join<D, 8>), a, s, q,
+               kp, vp, o, lse, parts, err, st);
+  if (rows <= 16) {
+    constexpr int ST2 = D == 128 ? 8 : ST;                // room for 16 rows of four warps
+    return run(paged_step_kernel<D, 2, ST2>, 16, ring_bytes<D, ST2>() + sizeof(Join<D, 16>), a, s,
+               q, kp, vp, o, lse, parts, err, st);
+  }
+  return run(paged_few_kernel<D, ST>, 64, ring_bytes<D, ST>(), a, s, q, kp, vp, o, lse, parts, err,
+             st);
 }
 
 }  // namespace

@@ -476,3 +476,44 @@ def test_paged_nothing_to_do(msa):
         pad.attn(msa, ws=torch.empty(512, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         pad.attn(msa, max_new=0)
+
+
+@pytest.mark.parametrize("new,hq", [(1, 32), (2, 64), (5, 32)])
+def test_paged_attn_long_caches_many_rounds(msa, new, hq):
+    """Rings that go round hundreds of times, with copies that arrive late and out of order (a
+    pool of 1.2 GB in shuffled small pages): every row against float64 on the GPU, five times."""
+    n, hkv, page, d, L = 40, 8, 16, 128, 7000
+    G, need = hq // hkv, -(-L // page)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    kp, vp = (torch.randn(n * need, hkv, page, d, generator=g, device="cuda",
+                          dtype=torch.bfloat16) for _ in range(2))
+    table = torch.randperm(n * need, generator=g, device="cuda").int().view(n, need)
+    lens = torch.randint(L - 500, L + 1, (n,), generator=g, device="cuda").int()
+    cu = torch.arange(0, (n + 1) * new, new, device="cuda").int()
+    q = (2 * torch.randn(n * new, hq, d, generator=g, device="cuda")).bfloat16()
+    ws = msa.paged_workspace(q, kp, lens)
+    o, lse = msa.paged_attn_fwd(q, kp, vp, table, lens, cu, max_new=new, ws=ws)
+    for _ in range(5):
+        o2, lse2 = msa.paged_attn_fwd(q, kp, vp, table, lens, cu, max_new=new, ws=ws)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert msa.read_device_error(ws) == 0
+    for s in range(n):
+        c = int(lens[s])
+        K, V = (x[table[s].long()].transpose(0, 1).reshape(hkv, -1, d)[:, :c].double()
+                for x in (kp, vp))
+        qs = q[s * new:(s + 1) * new].view(new, hkv, G, d).permute(1, 0, 2, 3).double()
+        x = (qs.reshape(hkv, new * G, d) @ K.transpose(1, 2)).view(hkv, new, G, c) * d ** -0.5
+        pos = torch.arange(c - new, c, device="cuda")
+        x.masked_fill_((torch.arange(c, device="cuda")[None] > pos[:, None])[None, :, None],
+                       -float("inf"))
+        z = x.logsumexp(-1)
+        p = torch.exp(x - z[..., None]).reshape(hkv, new * G, c)
+        ref, a = (p @ V).view(hkv, new, G, d), (p @ V.abs()).view(hkv, new, G, d)
+        big = (qs.abs().reshape(hkv, new * G, d) @ K.abs().transpose(1, 2)).amax(-1)
+        e = 4 * d * U * float(big.max()) * d ** -0.5
+        got = o[s * new:(s + 1) * new].view(new, hkv, G, d).permute(1, 0, 2, 3).double()
+        bound = 2.0 ** -8 * ref.abs() + a * (2 * e + 2.0 ** -19 + 2.0 ** -8 + 2 * c * U)
+        assert ((got - ref).abs() <= bound).all()
+        gl = lse[s * new:(s + 1) * new].view(new, hkv, G).permute(1, 0, 2).double()
+        assert ((gl - z).abs() <= e + 2.0 ** -20 + c * U + 4 * U * z.abs()).all()
