@@ -73,6 +73,10 @@ int paged_grid();                     // CTAs of a schedule: one an SM
 cudaError_t launch_paged_few(const HeadShape& s, PagedAttn a, int rows, const void* q,
                              const void* kp, const void* vp, void* o, float* lse,
                              const struct PagedParts& parts, int* err, cudaStream_t st);
+// chunk: bf16 on the tensor cores, row tiles of 2 x 128 rows.
+cudaError_t launch_paged_chunk(const HeadShape& s, PagedAttn a, const void* q, const void* kp,
+                               const void* vp, void* o, float* lse,
+                               const struct PagedParts& parts, int* err, cudaStream_t st);
 cudaError_t launch_paged_simt(const HeadShape& s, PagedAttn a, int rows, const void* q,
                               const void* kp, const void* vp, void* o, float* lse,
                               const struct PagedParts& parts, int* err, cudaStream_t st);

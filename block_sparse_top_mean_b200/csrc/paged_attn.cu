@@ -137,7 +137,9 @@ cudaError_t launch_paged_attn(const HeadShape& s, const PagedShape& g, int64_t m
   const PagedParts parts = parts_of(ws);
   if (s.dtype == MSA_F32)
     return launch_paged_simt(s, a, rows <= 16 ? 16 : 64, q, kp, vp, o, lse, parts, err, st);
-  return launch_paged_few(s, a, rows <= 16 ? (int)rows : 64, q, kp, vp, o, lse, parts, err, st);
+  if (rows <= 64 || scale < 0.f)       // (the chunk kernel takes maxima of unscaled scores)
+    return launch_paged_few(s, a, rows <= 16 ? (int)rows : 64, q, kp, vp, o, lse, parts, err, st);
+  return launch_paged_chunk(s, a, q, kp, vp, o, lse, parts, err, st);
 }
 
 }  // namespace msa

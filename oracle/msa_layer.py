@@ -78,7 +78,7 @@ def paged_append(k_pages, v_pages, k, v, table, kv_lens, cu, page, base=None, wk
 def paged_attention(q, k_pages, v_pages, table, kv_lens, cu, page, scale):
     """(o [T, hq, d], lse [T, hq], a [T, hq, d], s [T, hq]) of the step's tokens: causal
     attention over each sequence's cache.  a = sum_i softmax_i |v_i| and s = the largest
-    scale * sum |q_j k_ij| of a visible key are what error bounds are made of.  Rows of no
+    |scale| * sum |q_j k_ij| of a visible key are what error bounds are made of.  Rows of no
     sequence stay NaN; a row that sees nothing has o = 0, lse = -inf.  A table entry that is
     no page reads as zeros; keys past the table row do not exist."""
     T, hq, d = q.shape
@@ -109,5 +109,5 @@ def paged_attention(q, k_pages, v_pages, table, kv_lens, cu, page, scale):
                 o[t, h] = p @ V[:see, h // G] / l
                 a[t, h] = p @ np.abs(V[:see, h // G]) / l
                 lse[t, h] = m + np.log(l)
-                big[t, h] = scale * (np.abs(K[:see, h // G]) @ np.abs(q[t, h])).max()
+                big[t, h] = abs(scale) * (np.abs(K[:see, h // G]) @ np.abs(q[t, h])).max()
     return o, lse, a, big

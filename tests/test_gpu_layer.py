@@ -224,7 +224,7 @@ class Step:
         n = self.cu[-1]
         ref, rl, a, s = oracle.paged_attention(
             _np(self.q), _np(self.kp), _np(self.vp), self.table, self.kv, self.cu, self.page, scale)
-        e = 4 * self.d * U * s[:n]
+        e = 4 * self.d * U * np.abs(s[:n])
         keys = np.concatenate([np.zeros(0)] + [np.full(c, L) for c, L in zip(self.new, self.kv)])
         keys = np.maximum(keys, 0)[:, None]
         bf = self.dtype == torch.bfloat16
@@ -294,6 +294,13 @@ def test_paged_attn_strided_queries_scale_and_no_lse(msa):
     o, lse = msa.paged_attn_fwd(wide[:, 3:11], st.kp, st.vp, *st.dev, scale=0.05, want_lse=False)
     assert lse is None
     st.check(o, None, 0.05)
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 1.0])
+def test_paged_attn_any_scale(msa, scale):
+    for dtype in (torch.bfloat16, torch.float32):
+        st = Step(dtype, 64, 4, 2, 32, [(70, 150), (1, 40)])
+        st.check(*st.attn(msa, scale=scale), scale)
 
 
 def test_paged_attn_shared_prefix_and_many_sequences(msa):
