@@ -130,11 +130,53 @@ template <int KT>
 __device__ __forceinline__ int key_tiles(const PagedAttn& a, const SeqView& v, int rt) {
   return max(1, (tile_keys(a, v, rt) + KT - 1) / KT);
 }
+// sum_{i < n} floor((p i + q) / m) for 0 <= p, q and p (n - 1) + q < 2^31 (the Euclidean
+// algorithm on lattice points under a line: Graham, Knuth, Patashnik, Concrete Mathematics, 3.5).
+__device__ __forceinline__ int64_t floor_sum(int n, uint32_t m, uint32_t p, uint32_t q) {
+  int64_t sum = 0;
+  for (;;) {
+    if (p >= m) {
+      sum += (int64_t)n * (n - 1) / 2 * (p / m);
+      p %= m;
+    }
+    if (q >= m) {
+      sum += (int64_t)n * (q / m);
+      q %= m;
+    }
+    const uint64_t y = (uint64_t)p * n + q;               // height of the line's end
+    if (y < m) return sum;
+    n = (int)((uint32_t)y / m);
+    q = (uint32_t)y % m;
+    const uint32_t t = m;
+    m = p;
+    p = t;
+  }
+}
+// Cost of the first k row tiles of one KV head of a sequence: their key tiles and leads.  Row
+// tile i ends at key min(past + (i + 1) tt, cap): up to KT keys count as one tile, those that
+// reach cap as many as cap fills, the ones between as ceil of an arithmetic progression.
+template <int KT>
+__device__ __forceinline__ int64_t rows_cost(const PagedAttn& a, const SeqView& v, int k) {
+  if (k <= 4) {                       // (a generated token, a short chunk)
+    int64_t t = (int64_t)k * a.lead;
+    for (int rt = 0; rt < k; ++rt) t += key_tiles<KT>(a, v, rt);
+    return t;
+  }
+  const int64_t past = v.past;
+  // row tiles that end at or before KT, and before cap
+  const int64_t one = min((int64_t)k, max((int64_t)0, (KT - past) / a.tt));
+  const int64_t to = min((int64_t)k, max(one, (max((int64_t)0, v.cap - past) + a.tt - 1) / a.tt - 1));
+  const int full = max(1, (v.cap + KT - 1) / KT);
+  int64_t t = (int64_t)k * a.lead;
+  if (v.cap <= KT) return t + k;      // every row tile counts one
+  t += one + (k - to) * full;
+  if (to > one)
+    t += floor_sum((int)(to - one), KT, a.tt, (uint32_t)(past + (one + 1) * a.tt + KT - 1));
+  return t;
+}
 template <int KT>
 __device__ __forceinline__ int64_t group_cost(const PagedAttn& a, const SeqView& v) {
-  int64_t t = (int64_t)v.n_rt * a.lead;
-  for (int rt = 0; rt < v.n_rt; ++rt) t += key_tiles<KT>(a, v, rt);
-  return t;
+  return rows_cost<KT>(a, v, v.n_rt);
 }
 
 // A CTA's run [at, end) of the line and the item it is in: `tiles` tiles from `start` + lead on
@@ -205,12 +247,20 @@ __device__ __forceinline__ Run paged_plan(const PagedAttn& a, PlanSmem* sm) {
       const int64_t per = mine / a.hkv;
       r.g = (int)((w0 - lo) / per);
       r.start = lo + r.g * per;
-      r.rt = 0;
-      r.tiles = key_tiles<KT>(a, r.v, 0);
-      while (w0 >= r.start + a.lead + r.tiles) {
-        r.start += a.lead + r.tiles;
-        r.tiles = key_tiles<KT>(a, r.v, ++r.rt);
+      // the last row tile that starts at or before w0
+      int rt = 0, n_rt = r.v.n_rt;
+      while (n_rt > 1) {
+        const int half = n_rt / 2;
+        if (r.start + rows_cost<KT>(a, r.v, rt + half) <= w0) {
+          rt += half;
+          n_rt -= half;
+        } else {
+          n_rt = half;
+        }
       }
+      r.start += rows_cost<KT>(a, r.v, rt);
+      r.rt = rt;
+      r.tiles = key_tiles<KT>(a, r.v, rt);
       sm->run = r;
     }
     if (before > w0) break;

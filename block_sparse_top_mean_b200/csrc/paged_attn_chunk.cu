@@ -31,16 +31,19 @@ using namespace fastmath;
 
 constexpr int KT = 128;               // keys of a tile
 constexpr int kHalfRows = 128;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;        // two softmax warpgroups; issuer, producer, two spare warps
 constexpr int kIssuer = 8, kProducer = 9;
 constexpr uint32_t kHalf = 128 * 128; // 128 rows x 64 dims
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.f;
+#ifndef POLY
+#define POLY quintic_exp2x2
+#endif
 #ifndef CHUNK_LEAD
 #define CHUNK_LEAD 3
 #endif
 #ifndef CHUNK_POLY
-#define CHUNK_POLY 0x44
+#define CHUNK_POLY 0
 #endif
 constexpr int kLead = CHUNK_LEAD;
 constexpr int kPolyPairs = CHUNK_POLY;       // pairs of each 8 whose exponentials use the FMA pipe
@@ -51,7 +54,7 @@ template <int D> constexpr int kUnits = D == 128 ? 5 : 10;   // 160 KB
 template <int D>
 struct __align__(16) Shared {
   uint64_t kv_full[kUnits<D>], kv_empty[kUnits<D>];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_full[2], o_empty[2];
   uint32_t tmem;
   int abort;
   PlanSmem plan;
@@ -81,6 +84,95 @@ __device__ __forceinline__ int halves(const PagedAttn& a, const Run& r) {
   return r.v.n - r.rt * a.tt > a.tt / 2 ? 2 : 1;
 }
 
+// One row's softmax over a tile: scores (TMEM columns s_t ..) to weights (bf16, over them), the
+// row's reference and sum brought along.  lim: the tile's keys that the row sees; FULL: all, in
+// every row of the warp.  started: O (o_t ..) holds earlier tiles.  p_part[0] is arrived at when
+// the first half of the weights is in place, p_part[1] when all are.
+template <bool FULL, int D>
+__device__ __forceinline__ void softmax_tile(uint32_t s_t, uint32_t o_t, float c2, int lim,
+                                             bool started, float& mref, float& l,
+                                             uint64_t* p_part) {
+  uint32_t sv[4][32];
+  tmem_ld32(s_t, sv[0]);
+  tmem_ld32(s_t + 32, sv[1]);
+  tmem_ld_wait();
+  tmem_ld32(s_t + 64, sv[2]);
+  tmem_ld32(s_t + 96, sv[3]);
+  float mx = -CUDART_INF_F;
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    if (hf == 1) tmem_ld_wait();
+    if (FULL) {
+      float m8[8];                                        // eight chains of three-input maxima
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t* v = &sv[hf * 2 + (j >> 2)][(j & 3) * 8];
+        float m = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+        m = fmax3(m, __uint_as_float(v[3]), __uint_as_float(v[4]));
+        m = fmax3(m, __uint_as_float(v[5]), __uint_as_float(v[6]));
+        m8[j] = fmaxf(m, __uint_as_float(v[7]));
+      }
+      mx = fmax3(mx, fmax3(m8[0], m8[1], m8[2]),
+                 fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
+    } else {
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (hf * 64 + w * 32 + k < lim) mx = fmaxf(mx, __uint_as_float(sv[hf * 2 + w][k]));
+    }
+  }
+  const float mc = FULL || lim > 0 ? mx * c2 : -CUDART_INF_F;
+  const bool need = mc > mref + kRescaleLog2;
+  if (__any_sync(0xffffffffu, need)) {
+    const float f = need ? fast_exp2(mref - mc) : 1.f;
+    if (started) {                    // O holds the earlier tiles (s_full follows their products)
+#pragma unroll 1
+      for (int q = 0; q < D / 16; ++q) {
+        uint32_t ov[16];
+        tmem_ld16(o_t + q * 16, ov);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
+        tmem_st16(o_t + q * 16, ov);
+      }
+    }
+    l *= f;
+    if (need) mref = mc;
+  }
+  const float mb = mref > -CUDART_INF_F ? mref : 0.f;
+  float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      float x0, x1, p0, p1;
+      ffma2(x0, x1, __uint_as_float(sv[w][k]), __uint_as_float(sv[w][k + 1]), c2, c2, -mb, -mb);
+      if ((kPolyPairs >> ((k / 2) & 7)) & 1) {
+        POLY(x0, x1, p0, p1);
+      } else {
+        p0 = fast_exp2(x0);
+        p1 = fast_exp2(x1);
+      }
+      if (!FULL) {
+        p0 = w * 32 + k < lim ? p0 : 0.f;
+        p1 = w * 32 + k + 1 < lim ? p1 : 0.f;
+      }
+      if (w & 1) fadd2(a0, a1, a0, a1, p0, p1);
+      else fadd2(b0, b1, b0, b1, p0, p1);
+      pk[k / 2] = pack_bf16x2(p0, p1);
+    }
+    tmem_st16(s_t + w * 16, pk);                          // over scores already read
+    if (w & 1) {
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&p_part[w >> 1]);
+    }
+  }
+  l += (a0 + a1) + (b0 + b1);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -107,7 +199,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
     mbar_init(&sm.q_empty, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sm.s_full[x], 1);
-      mbar_init(&sm.p_full[x], kHalfRows);
+      mbar_init(&sm.p_full[x][0], kHalfRows);
+      mbar_init(&sm.p_full[x][1], kHalfRows);
       mbar_init(&sm.o_full[x], 1);
       mbar_init(&sm.o_empty[x], kHalfRows);
     }
@@ -122,7 +215,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-
+  // Registers: 168 a thread at launch (3 x 128 x 168); the softmax holds a row's 128 scores.
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == kProducer) {
     // ---------------------------------------------------------------- producer
     const int per = KT / box;                             // page pieces of a tile
@@ -214,7 +309,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
       return at;
     };
     auto issue_qk = [&](int x, int ku) {
-      if (lane == 0) {
+      if (elect_one()) {
         const uint64_t qd = qd0 + (uint64_t)(x * DH) * (kHalf >> 4);
         const uint64_t kd = kd0 + (uint64_t)ku * (kUnit<D> >> 4);
 #pragma unroll
@@ -234,7 +329,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
       if (!ok || !wait(sm, &sm.q_full, (uint32_t)item & 1, err)) break;
       tc_fence_after();
       for (int x = 0; x < nx; ++x) issue_qk(x, ku);
-      if (lane == 0) {
+      if (elect_one()) {
         umma_commit(&sm.kv_empty[ku]);
         if (nt == 1) umma_commit(&sm.q_empty);
       }
@@ -257,24 +352,27 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
         if (more) ku = take();
         if (!ok) break;
         for (int x = 0; x < nx && ok; ++x) {
-          ok = wait(sm, &sm.p_full[x], steps[x] & 1, err);
-          ++steps[x];
-          if (ok && i == 0) ok = wait(sm, &sm.o_empty[x], (done[x] & 1) ^ 1, err);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t vd = vd0 + (uint64_t)vu * (kUnit<D> >> 4);
+          if (i == 0 && !wait(sm, &sm.o_empty[x], (done[x] & 1) ^ 1, err)) { ok = false; break; }
 #pragma unroll
-            for (int s = 0; s < KT / 16; ++s)
-              umma_ts(tmem + 256 + x * 128, tmem + x * 128 + s * 8,
-                      vd + (uint64_t)(s * (2048 >> 4)), id_o, (i > 0 || s > 0) ? 1u : 0u);
-            if (!more) umma_commit(&sm.o_full[x]);
+          for (int hf = 0; hf < 2; ++hf) {                // the weights come in two parts
+            if (!wait(sm, &sm.p_full[x][hf], steps[x] & 1, err)) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t vd = vd0 + (uint64_t)vu * (kUnit<D> >> 4);
+#pragma unroll
+              for (int s = hf * 4; s < hf * 4 + 4; ++s)
+                umma_ts(tmem + 256 + x * 128, tmem + x * 128 + s * 8,
+                        vd + (uint64_t)(s * (2048 >> 4)), id_o, (i > 0 || s > 0) ? 1u : 0u);
+              if (!more && hf == 1) umma_commit(&sm.o_full[x]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
+          ++steps[x];
           if (more) issue_qk(x, ku);
           else ++done[x];
         }
-        if (lane == 0 && ok) {
+        if (ok && elect_one()) {
           umma_commit(&sm.kv_empty[vu]);
           if (more) umma_commit(&sm.kv_empty[ku]);
           if (i + 2 == nt) umma_commit(&sm.q_empty);
@@ -283,13 +381,16 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
       }
       ++item;
     } while (ok && run_next<KT>(a, r));
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---------------------------------------------------------------- softmax, epilogue
     const int x = warp >> 2, row = tid & 127;             // this warpgroup's half, this row
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_t = lanes + x * 128, o_t = lanes + 256 + x * 128;
     const int half_toks = a.tt / 2, in_half = row / a.G, h = row - in_half * a.G;
     const float c2 = a.scale_log2;
+    const bool wide = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
     uint32_t steps = 0, items = 0;
     bool first_item = true, ok = true;
     do {
@@ -307,100 +408,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
           const int lim = (int)max(0LL, min((long long)KT, see - (long long)(tile0 + i) * KT));
           if (!wait(sm, &sm.s_full[x], steps & 1, err)) { ok = false; break; }
           tc_fence_after();
-          const bool full = __all_sync(0xffffffffu, lim == KT);
-          float sum = 0.f;
-          // two halves of 64 columns: a half's maximum comes from the registers just loaded
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t sv[2][32];
-            tmem_ld32(s_t + hf * 64, sv[0]);
-            tmem_ld32(s_t + hf * 64 + 32, sv[1]);
-            tmem_ld_wait();
-            float mx = -CUDART_INF_F;
-            if (full) {
-              float m8[8];                                // eight chains of three-input maxima
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const uint32_t* v = &sv[j >> 2][(j & 3) * 8];
-                float m = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
-                m = fmax3(m, __uint_as_float(v[3]), __uint_as_float(v[4]));
-                m = fmax3(m, __uint_as_float(v[5]), __uint_as_float(v[6]));
-                m8[j] = fmaxf(m, __uint_as_float(v[7]));
-              }
-              mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
-                         fmaxf(m8[6], m8[7]));
-            } else {
-#pragma unroll
-              for (int w = 0; w < 2; ++w)
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (hf * 64 + w * 32 + k < lim) mx = fmaxf(mx, __uint_as_float(sv[w][k]));
-            }
-            const float mc = lim > hf * 64 ? mx * c2 : -CUDART_INF_F;
-            const bool need = mc > mref + kRescaleLog2;
-            if (__any_sync(0xffffffffu, need)) {
-              const float f = need ? fast_exp2(mref - mc) : 1.f;
-              if (i > 0) {                                // O holds the earlier tiles (s_full
-#pragma unroll 1                                          // follows their products)
-                for (int q = 0; q < D / 16; ++q) {
-                  uint32_t ov[16];
-                  tmem_ld16(o_t + q * 16, ov);
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
-                  tmem_st16(o_t + q * 16, ov);
-                }
-                tmem_st_wait();
-              }
-              if (hf == 1) {                              // the first half of this tile's P
-                tmem_st_wait();
-#pragma unroll 1
-                for (int q = 0; q < 2; ++q) {
-                  uint32_t pv[16];
-                  tmem_ld16(s_t + q * 16, pv);
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int k = 0; k < 16; ++k)
-                    pv[k] = pack_bf16x2(bf16lo_to_f32(pv[k]) * f, bf16hi_to_f32(pv[k]) * f);
-                  tmem_st16(s_t + q * 16, pv);
-                }
-              }
-              l *= f;
-              sum *= f;
-              if (need) mref = mc;
-            }
-            const float mb = mref > -CUDART_INF_F ? mref : 0.f;
-            uint32_t pk[32];
-            float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                float x0, x1, p0, p1;
-                ffma2(x0, x1, __uint_as_float(sv[w][k]), __uint_as_float(sv[w][k + 1]), c2, c2,
-                      -mb, -mb);
-                if ((kPolyPairs >> ((k / 2) & 7)) & 1) {
-                  quintic_exp2x2(x0, x1, p0, p1);
-                } else {
-                  p0 = fast_exp2(x0);
-                  p1 = fast_exp2(x1);
-                }
-                if (!full) {
-                  const int kk = hf * 64 + w * 32 + k;
-                  p0 = kk < lim ? p0 : 0.f;
-                  p1 = kk + 1 < lim ? p1 : 0.f;
-                }
-                if (w == 0) fadd2(a0, a1, a0, a1, p0, p1);
-                else fadd2(b0, b1, b0, b1, p0, p1);
-                pk[w * 16 + k / 2] = pack_bf16x2(p0, p1);
-              }
-            sum += (a0 + a1) + (b0 + b1);
-            tmem_st32(s_t + hf * 32, pk);                 // over columns already read
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(&sm.p_full[x]);
-          l += sum;
+          // (two bodies: with the mask's comparisons in one, every column paid for them)
+          if (__all_sync(0xffffffffu, lim == KT))
+            softmax_tile<true, D>(s_t, o_t, c2, lim, i > 0, mref, l, sm.p_full[x]);
+          else
+            softmax_tile<false, D>(s_t, o_t, c2, lim, i > 0, mref, l, sm.p_full[x]);
         }
         if (!ok || !wait(sm, &sm.o_full[x], items & 1, err)) { ok = false; break; }
         tc_fence_after();
@@ -415,22 +427,28 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
           tmem_ld32(o_t + q * 32, ov);
           tmem_ld_wait();
           if (!on) continue;
+          // (32 bytes a store: a warp's rows are D elements apart, and each store of 16 would
+          // touch the same 32 lines again)
           if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(o + qrow * D + q * 32);
+            __nv_bfloat16* dst = o + qrow * D + q * 32;
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
+            for (int e = 0; e < 16; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(ov[2 * e]) * inv,
+                                 __uint_as_float(ov[2 * e + 1]) * inv);
+            if (wide) {
+              st_global_v8(dst, w);
+              st_global_v8(dst + 16, w + 8);
+            } else {
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16x2(__uint_as_float(ov[k * 8 + 2 * e]) * inv,
-                                   __uint_as_float(ov[k * 8 + 2 * e + 1]) * inv);
-              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(dst)[e] =
+                    make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
             }
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(parts.o + (slot * kPagedMaxRows + prow) * D + q * 32);
+            float* dst = parts.o + (slot * kPagedMaxRows + prow) * D + q * 32;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              dst[k] = make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+            for (int k = 0; k < 4; ++k) st_global_v8(dst + 8 * k, ov + 8 * k);
           }
         }
         tc_fence_before();
