@@ -23,6 +23,8 @@
 
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace msa {
@@ -68,6 +70,9 @@ struct PagedAttn {
 
 size_t paged_attn_ws_bytes(const HeadShape& s);
 int paged_grid();                     // CTAs of a schedule: one an SM
+// Raises a kernel's shared memory limit on the current device, once (done: the kernel's own
+// record of the devices where that happened).
+cudaError_t raise_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>* done);
 // Each kernel takes the sequences with a.min_new .. a.max_new new tokens, whatever their rows.
 // rows: the row tile asked for (at least G).  few: bf16; simt: fp32.
 cudaError_t launch_paged_few(const HeadShape& s, PagedAttn a, int rows, const void* q,

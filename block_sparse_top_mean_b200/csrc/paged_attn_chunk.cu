@@ -486,8 +486,8 @@ cudaError_t run(PagedAttn& a, const HeadShape& s, const void* q, const void* kp,
       !make_bf16_2d_map(&mk, kp, pool, D, box) || !make_bf16_2d_map(&mv, vp, pool, D, box))
     return cudaErrorInvalidValue;
   const size_t smem = 1024 + 2 * (D / 64) * kHalf + kUnits<D> * kUnit<D> + sizeof(Shared<D>);
-  cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = raise_smem((const void*)paged_chunk_kernel<D>, smem, &done);
   if (e != cudaSuccess) return e;
   const int grid = paged_grid();
   paged_chunk_kernel<D><<<grid, kThreads, smem, st>>>(mq, mk, mv, box, (__nv_bfloat16*)o, lse,

@@ -617,7 +617,7 @@ template <int D, int ST>
 constexpr size_t ring_bytes() { return 1024 + ST * kStageBytes<D> + sizeof(Ring<D, ST>); }
 
 template <typename K>
-cudaError_t run(K kernel, int rows, size_t smem, PagedAttn& a, const HeadShape& s, const void* q,
+cudaError_t run(K kernel, std::atomic<uint64_t>* done, int rows, size_t smem, PagedAttn& a, const HeadShape& s, const void* q,
                 const void* kp, const void* vp, void* o, float* lse, const PagedParts& parts,
                 int* err, cudaStream_t st) {
   a.tt = rows / a.G;
@@ -627,8 +627,7 @@ cudaError_t run(K kernel, int rows, size_t smem, PagedAttn& a, const HeadShape& 
   CUtensorMap mk{}, mv{};
   if (!make_bf16_2d_map(&mk, kp, pool, s.d, box) || !make_bf16_2d_map(&mv, vp, pool, s.d, box))
     return cudaErrorInvalidValue;
-  cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = raise_smem((const void*)kernel, smem, done);
   if (e != cudaSuccess) return e;
   const int grid = paged_grid();
   kernel<<<grid, kThreads, smem, st>>>(mk, mv, box, (const __nv_bfloat16*)q, (__nv_bfloat16*)o,
@@ -642,15 +641,16 @@ cudaError_t run_rows(int rows, PagedAttn& a, const HeadShape& s, const void* q, 
                      const void* vp, void* o, float* lse, const PagedParts& parts, int* err,
                      cudaStream_t st) {
   constexpr int ST = FEW_ST * 128 / D;                    // 192 KB of tiles
+  static std::atomic<uint64_t> done[3];
   if (rows <= 8)
-    return run(paged_step_kernel<D, 1, ST>, 8, ring_bytes<D, ST>() + sizeof(Join<D, 8>), a, s, q,
+    return run(paged_step_kernel<D, 1, ST>, &done[0], 8, ring_bytes<D, ST>() + sizeof(Join<D, 8>), a, s, q,
                kp, vp, o, lse, parts, err, st);
   if (rows <= 16) {
     constexpr int ST2 = D == 128 ? 8 : ST;                // room for 16 rows of four warps
-    return run(paged_step_kernel<D, 2, ST2>, 16, ring_bytes<D, ST2>() + sizeof(Join<D, 16>), a, s,
+    return run(paged_step_kernel<D, 2, ST2>, &done[1], 16, ring_bytes<D, ST2>() + sizeof(Join<D, 16>), a, s,
                q, kp, vp, o, lse, parts, err, st);
   }
-  return run(paged_few_kernel<D, ST>, 64, ring_bytes<D, ST>(), a, s, q, kp, vp, o, lse, parts, err,
+  return run(paged_few_kernel<D, ST>, &done[2], 64, ring_bytes<D, ST>(), a, s, q, kp, vp, o, lse, parts, err,
              st);
 }
 

@@ -156,8 +156,8 @@ cudaError_t run(PagedAttn& a, const HeadShape& s, const void* q, const void* kp,
   a.tt = ROWS / a.G;
   a.lead = 1;
   const size_t smem = sizeof(Smem<D, ROWS>);
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_simt_kernel<T, D, ROWS>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = raise_smem((const void*)paged_attn_simt_kernel<T, D, ROWS>, smem, &done);
   if (e != cudaSuccess) return e;
   const int grid = paged_grid();
   paged_attn_simt_kernel<T, D, ROWS><<<grid, ROWS * kLanes, smem, st>>>(

@@ -17,75 +17,86 @@ from . import _lib
 from ._lib import MSA_BF16, MSA_F32, MsaError, MsaPagedCache, MsaParams
 
 _DT = {torch.float32: MSA_F32, torch.bfloat16: MSA_BF16}
+_I32, _F32 = torch.int32, torch.float32
 _byref = ctypes.byref
+_fns = {}
 
 
 def _fail(text):
     raise ValueError(text)
 
 
-def _call(name, device, *args):
-    """The library's entry on `device`'s current stream (launches need it to be current)."""
-    fn = getattr(_lib.load(), name)
-    # the raw handle: building a torch.cuda.Stream object costs 2 us of a 10 us call
-    stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
+def _call(name, index, *args):
+    """The library's entry on the current stream of device `index` (launches need that device to
+    be current).  These calls often take less time on the GPU than on the host, so the host
+    side looks names up once and asks for the raw stream handle (a torch.cuda.Stream object
+    costs 2 us)."""
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(_lib.load(), name)
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
         st = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             st = fn(*args, stream)
     if st != 0:
         _lib.check(name, st)
 
 
-def _rows(name, x, d, dtype, device):
+def _device(name, x):
+    """Index of x's CUDA device; x must be float32 or bfloat16."""
+    index = x.get_device()
+    if index < 0:
+        _fail(f"{name}: block_sparse_top_mean_b200 takes CUDA tensors only")
+    if x.dtype not in _DT:
+        _fail(f"{name} must be float32 or bfloat16")
+    return index
+
+
+def _rows(name, x, T, d, dtype, index):
     """Checks x [T, heads, d] with packed heads and returns its token stride."""
-    if x.dtype != dtype or x.device != device:
-        _fail(f"{name} must be {dtype} on {device}")
-    if x.dim() != 3 or x.shape[2] != d:
-        _fail(f"{name} must be [tokens, heads, {d}]")
-    T, h, _ = x.shape
-    s0, s1, s2 = x.stride()
-    if (s2 != 1 or (s1 != d and h > 1)) and x.numel():
-        _fail(f"{name}: the heads of a token must be packed (only the token stride is free)")
-    return s0 if T > 1 else h * d
+    if x.dtype is not dtype or x.get_device() != index:
+        _fail(f"{name} must be {dtype} on cuda:{index}")
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or shape[2] != d or shape[0] != T:
+        _fail(f"{name} must be [{T}, heads, {d}]")
+    if stride[2] != 1 or stride[1] != d:
+        if x.numel() and (stride[2] != 1 or shape[1] > 1):
+            _fail(f"{name}: the heads of a token must be packed (only the token stride is free)")
+    return stride[0] if T > 1 else shape[1] * d
 
 
-def _ints(name, x, shape, device):
-    if x.dtype != torch.int32 or x.device != device or not x.is_contiguous():
-        _fail(f"{name} must be a contiguous int32 tensor on {device}")
-    if x.dim() != len(shape) or any(b is not None and a != b for a, b in zip(x.shape, shape)):
-        _fail(f"{name} must have shape {shape}")
+def _ints(name, x, index):
+    """Pointer of a contiguous int32 tensor."""
+    if x.dtype is not _I32 or x.get_device() != index or not x.is_contiguous():
+        _fail(f"{name} must be a contiguous int32 tensor on cuda:{index}")
+    return x.data_ptr()
 
 
-def _weight(name, w, d, dtype, device):
+def _weight(name, w, d, dtype, index):
     if w is None:
         return None
-    if w.dtype != dtype or w.device != device or w.shape != (d,) or not w.is_contiguous():
-        _fail(f"{name} must be a contiguous [{d}] {dtype} tensor on {device}")
+    if w.dtype is not dtype or w.get_device() != index or w.shape != (d,) or \
+            not w.is_contiguous():
+        _fail(f"{name} must be a contiguous [{d}] {dtype} tensor on cuda:{index}")
     return w.data_ptr()
 
 
-def _out(name, x, shape, dtype, device):
-    if x is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if x.dtype != dtype or x.device != device or tuple(x.shape) != tuple(shape) or \
+def _packed(name, x, shape, dtype, index):
+    if x.dtype is not dtype or x.get_device() != index or x.shape != shape or \
             not x.is_contiguous():
-        _fail(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
+        _fail(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on cuda:{index}")
     return x
 
 
-def _head_shape(q, k):
-    if not q.is_cuda:
-        _fail("block_sparse_top_mean_b200 takes CUDA tensors only")
-    if q.dtype not in _DT:
-        _fail("tensors must be float32 or bfloat16")
-    if q.dim() != 3 or k.dim() != 3:
-        _fail("q and k must be [tokens, heads, d]")
-    T, hq, d = q.shape
-    if k.shape[0] != T:
-        _fail("q and k must hold the same tokens")
-    return T, hq, k.shape[1], d
+def _like(name, x, src, dtype, index):
+    """x checked, or a new packed tensor of src's shape."""
+    if x is not None:
+        return _packed(name, x, src.shape, dtype, index)
+    if src.dtype is dtype:
+        return torch.empty_like(src, memory_format=torch.contiguous_format)
+    return src.new_empty(src.shape, dtype=dtype)
 
 
 def _workspace(p, op, device):
@@ -97,20 +108,24 @@ def _workspace(p, op, device):
     return ws
 
 
-def _ws_ptr(ws, device):
-    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
-        _fail(f"ws must be a contiguous uint8 tensor on {device}")
+def _ws_ptr(ws, index):
+    if ws.dtype is not torch.uint8 or ws.get_device() != index or not ws.is_contiguous():
+        _fail(f"ws must be a contiguous uint8 tensor on cuda:{index}")
     return ws.data_ptr(), ws.numel()
 
 
 def _norm_args(q, k, cu_seqlens, wq, wk):
-    T, hq, hkv, d = _head_shape(q, k)
-    dt, dev = q.dtype, q.device
-    qs, ks = _rows("q", q, d, dt, dev), _rows("k", k, d, dt, dev)
-    _ints("cu_seqlens", cu_seqlens, (None,), dev)
-    p = MsaParams(1, T, hq, hkv, d, 1, 1, 1.0, _DT[dt])
-    return (p, dev, dt, (T, hq, d), (T, hkv, d), qs, ks, _weight("wq", wq, d, dt, dev),
-            _weight("wk", wk, d, dt, dev))
+    index, dt = _device("q", q), q.dtype
+    if q.dim() != 3 or k.dim() != 3:
+        _fail("q and k must be [tokens, heads, d]")
+    T, hq, d = q.shape
+    qs, ks = _rows("q", q, T, d, dt, index), _rows("k", k, T, d, dt, index)
+    if cu_seqlens.dim() != 1:
+        _fail("cu_seqlens must have one dimension")
+    cu = _ints("cu_seqlens", cu_seqlens, index)
+    p = MsaParams(1, T, hq, k.shape[1], d, 1, 1, 1.0, _DT[dt])
+    return (p, index, dt, cu, cu_seqlens.shape[0] - 1, qs, ks, _weight("wq", wq, d, dt, index),
+            _weight("wk", wk, d, dt, index))
 
 
 def qk_norm_rope(q, k, cu_seqlens, base: float, wq=None, wk=None, eps: float = 1e-6, out=None):
@@ -119,18 +134,19 @@ def qk_norm_rope(q, k, cu_seqlens, base: float, wq=None, wk=None, eps: float = 1
     (cu_seqlens: int32 CUDA tensor of the n_docs + 1 boundaries).  q and k may be strided in
     the token dimension (views of a fused projection).  Returns (q_out, k_out), packed; `out`
     may pass them, or q and k themselves when those are packed."""
-    p, dev, dt, sq, sk, qs, ks, pq, pk = _norm_args(q, k, cu_seqlens, wq, wk)
-    qo = _out("q_out", None if out is None else out[0], sq, dt, dev)
-    ko = _out("k_out", None if out is None else out[1], sk, dt, dev)
-    _call("msa_qk_norm_rope", dev, _byref(p), cu_seqlens.data_ptr(), cu_seqlens.numel() - 1,
-          q.data_ptr(), qs, k.data_ptr(), ks, pq, pk, base, eps, qo.data_ptr(), ko.data_ptr())
+    p, index, dt, cu, n, qs, ks, pq, pk = _norm_args(q, k, cu_seqlens, wq, wk)
+    qo = _like("q_out", None if out is None else out[0], q, dt, index)
+    ko = _like("k_out", None if out is None else out[1], k, dt, index)
+    _call("msa_qk_norm_rope", index, _byref(p), cu, n, q.data_ptr(), qs, k.data_ptr(), ks, pq, pk,
+          base, eps, qo.data_ptr(), ko.data_ptr())
     return qo, ko
 
 
 def qk_norm_rope_workspace(q, k):
     """A workspace for qk_norm_rope_bwd (it depends on the head shape alone)."""
-    T, hq, hkv, d = _head_shape(q, k)
-    return _workspace(MsaParams(1, T, hq, hkv, d, 1, 1, 1.0, _DT[q.dtype]),
+    _device("q", q)
+    T, hq, d = q.shape
+    return _workspace(MsaParams(1, T, hq, k.shape[1], d, 1, 1, 1.0, _DT[q.dtype]),
                       _lib.OP_QK_NORM_ROPE_BWD, q.device)
 
 
@@ -139,47 +155,50 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, cu_seqlens, base: float, wq=None, wk=
     """Gradient of qk_norm_rope for the upstream gradients dq_out, dk_out (packed; fp32 or the
     inputs' dtype): (dq, dk, dwq, dwk), dq and dk in the inputs' dtype, the weights' gradients
     in fp32.  `out` may pass the four tensors."""
-    p, dev, dt, sq, sk, qs, ks, pq, pk = _norm_args(q, k, cu_seqlens, wq, wk)
+    p, index, dt, cu, n, qs, ks, pq, pk = _norm_args(q, k, cu_seqlens, wq, wk)
     gt = dq_out.dtype
-    if gt not in (torch.float32, dt):
+    if gt is not dt and gt is not _F32:
         _fail(f"the upstream gradients must be float32 or {dt}")
-    _out("dq_out", dq_out, sq, gt, dev)
-    _out("dk_out", dk_out, sk, gt, dev)
+    _packed("dq_out", dq_out, q.shape, gt, index)
+    _packed("dk_out", dk_out, k.shape, gt, index)
     o = (None,) * 4 if out is None else out
-    d = sq[2]
-    dq, dk = _out("dq", o[0], sq, dt, dev), _out("dk", o[1], sk, dt, dev)
-    dwq, dwk = (_out(n, x, (d,), torch.float32, dev) for n, x in (("dwq", o[2]), ("dwk", o[3])))
+    dq, dk = _like("dq", o[0], q, dt, index), _like("dk", o[1], k, dt, index)
+    if out is None:
+        dwq, dwk = q.new_empty((2, p.d), dtype=_F32).unbind()
+    else:
+        dwq, dwk = (_packed(name, x, (p.d,), _F32, index) for name, x in
+                    (("dwq", o[2]), ("dwk", o[3])))
     if ws is None:
-        ws = _workspace(p, _lib.OP_QK_NORM_ROPE_BWD, dev)
-    wp, wn = _ws_ptr(ws, dev)
-    _call("msa_qk_norm_rope_bwd", dev, _byref(p), cu_seqlens.data_ptr(), cu_seqlens.numel() - 1,
-          dq_out.data_ptr(), dk_out.data_ptr(), _DT[gt], q.data_ptr(), qs, k.data_ptr(), ks, pq,
-          pk, base, eps, dq.data_ptr(), dk.data_ptr(), dwq.data_ptr(), dwk.data_ptr(), wp, wn)
+        ws = _workspace(p, _lib.OP_QK_NORM_ROPE_BWD, q.device)
+    wp, wn = _ws_ptr(ws, index)
+    _call("msa_qk_norm_rope_bwd", index, _byref(p), cu, n, dq_out.data_ptr(), dk_out.data_ptr(),
+          _DT[gt], q.data_ptr(), qs, k.data_ptr(), ks, pq, pk, base, eps, dq.data_ptr(),
+          dk.data_ptr(), dwq.data_ptr(), dwk.data_ptr(), wp, wn)
     return dq, dk, dwq, dwk
 
 
-def _cache(k_pages, v_pages, page_table, kv_lens, cu_seqlens, dtype, device):
+def _cache(k_pages, v_pages, page_table, kv_lens, cu_seqlens, dtype, index):
     """The checked cache of a step and its shape (n_seqs, hkv, page, d)."""
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+    shape = k_pages.shape
+    if len(shape) != 4 or shape != v_pages.shape:
         _fail("k_pages and v_pages must both be [n_pages, hkv, page, d]")
-    for name, x in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if x.dtype != dtype or x.device != device or not x.is_contiguous():
-            _fail(f"{name} must be a contiguous {dtype} tensor on {device}")
-    n_pages, hkv, page, d = k_pages.shape
-    _ints("kv_lens", kv_lens, (None,), device)
-    n = kv_lens.numel()
-    _ints("page_table", page_table, (n, None), device)
-    _ints("cu_seqlens", cu_seqlens, (n + 1,), device)
-    c = MsaPagedCache(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                      kv_lens.data_ptr(), cu_seqlens.data_ptr(), n_pages, page_table.shape[1])
-    return c, n, hkv, page, d
+    for x in (k_pages, v_pages):
+        if x.dtype is not dtype or x.get_device() != index or not x.is_contiguous():
+            _fail(f"k_pages and v_pages must be contiguous {dtype} tensors on cuda:{index}")
+    n, table = kv_lens.numel(), page_table.shape
+    if kv_lens.dim() != 1 or len(table) != 2 or table[0] != n or cu_seqlens.shape != (n + 1,):
+        _fail("kv_lens, page_table and cu_seqlens must be [n_seqs], [n_seqs, max_pages] and "
+              "[n_seqs + 1]")
+    c = MsaPagedCache(k_pages.data_ptr(), v_pages.data_ptr(),
+                      _ints("page_table", page_table, index), _ints("kv_lens", kv_lens, index),
+                      _ints("cu_seqlens", cu_seqlens, index), shape[0], table[1])
+    return c, n, shape[1], shape[2], shape[3]
 
 
 def paged_workspace(q, k_pages, kv_lens):
     """A workspace for paged_attn_fwd and paged_append (it depends on the head shape alone, so
     one serves every step; calls that overlap on the GPU need one each)."""
-    if not q.is_cuda or q.dtype not in _DT:
-        _fail("q must be a float32 or bfloat16 CUDA tensor")
+    _device("q", q)
     T, hq, d = q.shape
     _, hkv, page, _ = k_pages.shape
     p = MsaParams(kv_lens.numel(), T, hq, hkv, d, page, 1, 1.0, _DT[q.dtype])
@@ -195,35 +214,35 @@ def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None
     rotated to their positions; with `eps`, their heads are normalised first (weights wq, wk
     or None for ones).  Returns the new queries [T, hq, d], or None without q.  Tokens without
     a page are skipped and reported in ws, if given (read_device_error)."""
-    if not k.is_cuda or k.dtype not in _DT:
-        _fail("k must be a float32 or bfloat16 CUDA tensor")
-    dt, dev = k.dtype, k.device
-    c, n, hkv, page, d = _cache(k_pages, v_pages, page_table, kv_lens, cu_seqlens, dt, dev)
-    ks, vs = _rows("k", k, d, dt, dev), _rows("v", v, d, dt, dev)
+    index, dt = _device("k", k), k.dtype
+    c, n, hkv, page, d = _cache(k_pages, v_pages, page_table, kv_lens, cu_seqlens, dt, index)
     T = k.shape[0]
-    if k.shape[1] != hkv or v.shape != k.shape:
+    ks, vs = _rows("k", k, T, d, dt, index), _rows("v", v, T, d, dt, index)
+    if k.shape[1] != hkv or v.shape[1] != hkv:
         _fail("k and v must be [tokens, hkv, d] with the cache's hkv and d")
     hq, qs, qp, op, qo = hkv, 0, None, None, None
     if q is not None:
-        qs = _rows("q", q, d, dt, dev)
-        if q.shape[0] != T:
-            _fail("q, k and v must hold the same tokens")
+        qs = _rows("q", q, T, d, dt, index)
         hq = q.shape[1]
-        qo = _out("out", out, (T, hq, d), dt, dev)
+        qo = _like("out", out, q, dt, index)
         qp, op = q.data_ptr(), qo.data_ptr()
     elif out is not None or wq is not None:
         _fail("out and wq are for a call with q")
-    if eps is None and (wq is not None or wk is not None):
-        _fail("wq and wk need eps")
-    if eps is not None and not eps > 0:
+    if eps is None:
+        if wq is not None or wk is not None:
+            _fail("wq and wk need eps")
+        eps = 0.0
+    elif not eps > 0:
         _fail("eps must be positive (None: no norm)")
-    if base is not None and not base > 1:
+    if base is None:
+        base = 0.0
+    elif not base > 1:
         _fail("base must be above 1 (None: no rotation)")
-    wp, wn = (None, 0) if ws is None else _ws_ptr(ws, dev)
+    wp, wn = (None, 0) if ws is None else _ws_ptr(ws, index)
     p = MsaParams(n, T, hq, hkv, d, page, 1, 1.0, _DT[dt])
-    _call("msa_paged_append", dev, _byref(p), _byref(c), qp, qs, k.data_ptr(), ks, v.data_ptr(),
-          vs, _weight("wq", wq, d, dt, dev), _weight("wk", wk, d, dt, dev), base or 0.0,
-          eps or 0.0, op, wp, wn)
+    _call("msa_paged_append", index, _byref(p), _byref(c), qp, qs, k.data_ptr(), ks, v.data_ptr(),
+          vs, _weight("wq", wq, d, dt, index), _weight("wk", wk, d, dt, index), base, eps, op, wp,
+          wn)
     return qo
 
 
@@ -235,22 +254,29 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens, max_new
     meaning.  Returns (o [T, hq, d], lse [T, hq] fp32 or None); a token that sees no key gets
     o = 0, lse = -inf; packed tokens behind the last sequence are left as they are (`out` may
     pass o and lse)."""
-    if not q.is_cuda or q.dtype not in _DT or q.dim() != 3:
-        _fail("q must be a float32 or bfloat16 CUDA tensor [tokens, hq, d]")
-    dt, dev = q.dtype, q.device
-    c, n, hkv, page, d = _cache(k_pages, v_pages, page_table, kv_lens, cu_seqlens, dt, dev)
-    qs = _rows("q", q, d, dt, dev)
+    index, dt = _device("q", q), q.dtype
+    c, n, hkv, page, d = _cache(k_pages, v_pages, page_table, kv_lens, cu_seqlens, dt, index)
+    if q.dim() != 3:
+        _fail("q must be [tokens, hq, d]")
     T, hq, _ = q.shape
-    if max_new is not None and max_new < 1 and T:
+    qs = _rows("q", q, T, d, dt, index)
+    if max_new is None:
+        max_new = 0
+    elif max_new < 1 and T:
         _fail("max_new must be positive (None: unknown)")
-    o = _out("o", None if out is None else out[0], (T, hq, d), dt, dev)
-    lse = None
-    if want_lse and (out is None or out[1] is not None):
-        lse = _out("lse", None if out is None else out[1], (T, hq), torch.float32, dev)
+    o = _like("o", None if out is None else out[0], q, dt, index)
+    lse = lp = None
+    if want_lse:
+        if out is None:
+            lse = q.new_empty((T, hq), dtype=_F32)
+            lp = lse.data_ptr()
+        elif out[1] is not None:
+            lse = _packed("lse", out[1], (T, hq), _F32, index)
+            lp = lse.data_ptr()
     p = MsaParams(n, T, hq, hkv, d, page, 1, d ** -0.5 if scale is None else scale, _DT[dt])
     if ws is None:
-        ws = _workspace(p, _lib.OP_PAGED_ATTN, dev)
-    wp, wn = _ws_ptr(ws, dev)
-    _call("msa_paged_attn_fwd", dev, _byref(p), _byref(c), max_new or 0, q.data_ptr(), qs,
-          o.data_ptr(), None if lse is None else lse.data_ptr(), wp, wn)
+        ws = _workspace(p, _lib.OP_PAGED_ATTN, q.device)
+    wp, wn = _ws_ptr(ws, index)
+    _call("msa_paged_attn_fwd", index, _byref(p), _byref(c), max_new, q.data_ptr(), qs,
+          o.data_ptr(), lp, wp, wn)
     return o, lse
