@@ -197,7 +197,10 @@ size_t decode_ws_bytes(const Shape& s, int64_t n_query);   // header included
 // Host helpers (host_util.cu): a 2-D bf16 TMA map over a row-major [rows, cols] tensor
 // with 64-column x box_rows boxes and 128-byte swizzle; the device's SM count.
 bool make_bf16_2d_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows);
-// The same over [tokens, heads, d] with a token stride (elements): boxes of box_tokens tokens x
+// The same for either dtype: boxes of 128 bytes x box_rows.
+bool make_2d_map(CUtensorMap* m, const void* base, int dtype, int64_t rows, int64_t cols,
+                 int box_rows);
+// bf16 over [tokens, heads, d] with a token stride (elements): boxes of box_tokens tokens x
 // box_heads heads x 64 columns, one 128-byte row for each (token, head).
 bool make_bf16_heads_map(CUtensorMap* m, const void* base, int64_t tokens, int64_t heads,
                          int64_t d, int64_t stride, int box_heads, int box_tokens);

@@ -81,33 +81,5 @@ __device__ __forceinline__ void poly_exp2x2(float x0, float x1, float& p0, float
   p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
 }
 
-// The same reduction with the degree-5 minimax polynomial (relative error: optimum 7.49e-8,
-// 2.2e-7 with fp32 coefficients and evaluation).  Two more packed steps than the cubic, for
-// kernels whose log-sum-exp is held to fp32 accuracy.
-constexpr float kExpQ5 = 0.0013276472454890609f;
-constexpr float kExpQ4 = 0.009675540961325169f;
-constexpr float kExpQ3 = 0.05550713092088699f;
-constexpr float kExpQ2 = 0.24022120237350464f;
-constexpr float kExpQ1 = 0.6931469440460205f;
-constexpr float kExpQ0 = 1.0000001192092896f;
-
-__device__ __forceinline__ void quintic_exp2x2(float x0, float x1, float& p0, float& p1) {
-  constexpr float kShift = 12582912.f;            // 1.5 * 2^23
-  x0 = fmaxf(x0, -126.f);
-  x1 = fmaxf(x1, -126.f);
-  float t0, t1, n0, n1, f0, f1;
-  fadd2(t0, t1, x0, x1, kShift, kShift);
-  fadd2(n0, n1, t0, t1, -kShift, -kShift);        // exact: n as a float
-  ffma2(f0, f1, n0, n1, -1.f, -1.f, x0, x1);      // exact: x - n
-  float q0, q1;
-  ffma2(q0, q1, kExpQ5, kExpQ5, f0, f1, kExpQ4, kExpQ4);
-  ffma2(q0, q1, q0, q1, f0, f1, kExpQ3, kExpQ3);
-  ffma2(q0, q1, q0, q1, f0, f1, kExpQ2, kExpQ2);
-  ffma2(q0, q1, q0, q1, f0, f1, kExpQ1, kExpQ1);
-  ffma2(q0, q1, q0, q1, f0, f1, kExpQ0, kExpQ0);
-  p0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
-  p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
-}
-
 }  // namespace fastmath
 }  // namespace msa

@@ -108,7 +108,7 @@ size_t layer_ws_bytes(const msa_params* p, int32_t op) {
   if (check_heads(p, &s) != MSA_OK) return 0;
   switch (op) {
     case MSA_OP_QK_NORM_ROPE_BWD:
-      return kWsHeader + (size_t)qk_norm_rope_bwd_ctas() * 2 * s.d * sizeof(float);
+      return kWsHeader + (size_t)qk_norm_rope_bwd_ctas() * s.d * sizeof(float);
     case MSA_OP_PAGED_APPEND:
       return kWsHeader;
     case MSA_OP_PAGED_ATTN:

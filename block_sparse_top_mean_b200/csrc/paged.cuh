@@ -41,7 +41,7 @@ struct PagedShape {
   int64_t n_seqs, max_pages, n_pages, page;
 };
 
-// qk_norm_rope.cu.  part: [qk_norm_rope_bwd_ctas()][2][d] fp32.
+// qk_norm_rope.cu.  part: [qk_norm_rope_bwd_ctas()][d] fp32.
 int64_t qk_norm_rope_bwd_ctas();
 cudaError_t launch_qk_norm_rope(const HeadShape& s, const int32_t* cu, int64_t n_docs,
                                 const void* q, int64_t qs, const void* k, int64_t ks,
@@ -74,7 +74,7 @@ int paged_grid();                     // CTAs of a schedule: one an SM
 // record of the devices where that happened).
 cudaError_t raise_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>* done);
 // Each kernel takes the sequences with a.min_new .. a.max_new new tokens, whatever their rows.
-// rows: the row tile asked for (at least G).  few: bf16; simt: fp32.
+// rows: the row tile asked for (at least G).  few: bf16; f32: fp32.
 cudaError_t launch_paged_few(const HeadShape& s, PagedAttn a, int rows, const void* q,
                              const void* kp, const void* vp, void* o, float* lse,
                              const struct PagedParts& parts, int* err, cudaStream_t st);
@@ -82,7 +82,7 @@ cudaError_t launch_paged_few(const HeadShape& s, PagedAttn a, int rows, const vo
 cudaError_t launch_paged_chunk(const HeadShape& s, PagedAttn a, const void* q, const void* kp,
                                const void* vp, void* o, float* lse,
                                const struct PagedParts& parts, int* err, cudaStream_t st);
-cudaError_t launch_paged_simt(const HeadShape& s, PagedAttn a, int rows, const void* q,
+cudaError_t launch_paged_f32(const HeadShape& s, PagedAttn a, int rows, const void* q,
                               const void* kp, const void* vp, void* o, float* lse,
                               const struct PagedParts& parts, int* err, cudaStream_t st);
 cudaError_t launch_paged_combine(const HeadShape& s, const PagedAttn& a, int grid, int rows,
@@ -96,15 +96,17 @@ cudaError_t launch_paged_attn(const HeadShape& s, const PagedShape& g, int64_t m
 // Workspace of one of these operators (msa_workspace_bytes); 0 for invalid shapes.
 size_t layer_ws_bytes(const msa_params* p, int32_t op);
 
-constexpr int kPagedCtas = 160;       // most CTAs of a schedule (a B200 has 148 SMs)
-constexpr int kPagedMaxRows = 256;    // rows of the largest row tile
+constexpr int kPagedCtas = 160;       // most SMs a schedule uses (a B200 has 148)
+constexpr int kPagedRecs = 2 * kPagedCtas;       // most CTAs: two an SM with row tiles of 64
+constexpr int kPagedMaxRows = 256;    // rows of the largest row tile (one CTA an SM)
 
 // Workspace body: records, then (maximum, sum) and outputs of the parts.  CTA c's parts: 2c
-// (its first item) and 2c + 1 (its last, when that is another).
+// (its first item) and 2c + 1 (its last, when that is another).  Sized for one CTA an SM with
+// row tiles of kPagedMaxRows; smaller row tiles leave room for more CTAs.
 struct PagedParts {
-  int4* rec;                          // [kPagedCtas], see item_record
-  float2* ml;                         // [2 * kPagedCtas][rows]
-  float* o;                           // [2 * kPagedCtas][rows][d]
+  int4* rec;                          // [kPagedRecs], see item_record
+  float2* ml;                         // [2 * CTAs][rows]
+  float* o;                           // [2 * CTAs][rows][d]
 };
 
 // ------------------------------------------------------------------ device side

@@ -15,8 +15,8 @@
 namespace msa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kUnroll = 4;            // rows in flight per lane
+constexpr int kWarps = 2;             // 8 CTAs an SM: 57 us for 11.5K tokens, 60 with 8 warps a CTA
+constexpr int kUnroll = 4;            // row groups of the queries in flight per warp
 
 struct AppendArgs {
   Turns tn;
@@ -27,7 +27,7 @@ struct AppendArgs {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 8)
 paged_append_kernel(const T* q, const T* k, const T* v, const T* __restrict__ wq,
                     const T* __restrict__ wk, T* __restrict__ kp, T* __restrict__ vp, T* qo,
                     int* err, const __grid_constant__ AppendArgs a) {
@@ -38,94 +38,74 @@ paged_append_kernel(const T* q, const T* k, const T* v, const T* __restrict__ wq
   const int64_t t = unit / a.split;
   if (t >= a.n_tok) return;                               // whole warp
   const int part = (int)(unit - t * a.split);
-  const int hk = a.hq + a.hkv, heads = hk + a.hkv;        // rows: queries, keys, values
-  float cs[N], sn[N];
-  bool placed = false;
-  int64_t slot = -1;                                      // row of head 0 in the pools
-  for (int h0 = part * R::kRows; h0 < heads; h0 += a.split * R::kRows * kUnroll) {
-    uint4 ra[kUnroll], rb[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * a.split * R::kRows + sub;
-      if (h >= heads) continue;
-      const T* row = h < a.hq   ? q + t * a.qs + (int64_t)h * D
-                     : h < hk ? k + t * a.ks + (int64_t)(h - a.hq) * D
-                              : v + t * a.vs + (int64_t)(h - hk) * D;
-      ra[u] = ld16_once(row + c * N);
-      rb[u] = ld16_once(row + D / 2 + c * N);
+  const int gq = (a.hq + R::kRows - 1) / R::kRows, gk = (a.hkv + R::kRows - 1) / R::kRows;
+  int64_t slot = -1, pos = 0;                             // row of KV head 0 in the pools
+  bool placed = false, angles = false, mine = false;
+  float cs0[N], sn0[N];
+  auto find = [&]() {
+    if (placed) return;
+    placed = true;
+    const int s = warp_segment(a.g.cu, (int)a.g.n_seqs, t);
+    if (s < 0) return;                                    // behind the last sequence
+    mine = true;
+    const int64_t c0 = __ldg(a.g.cu + s), c1 = __ldg(a.g.cu + s + 1);
+    pos = (int64_t)__ldg(a.g.kv_lens + s) - (c1 - c0) + (t - c0);
+    if (pos >= 0 && pos < a.g.max_pages * a.g.page) {
+      const int64_t pg = __ldg(a.g.table + (int64_t)s * a.g.max_pages + pos / a.g.page);
+      if (pg >= 0 && pg < a.g.n_pages) slot = pg * a.hkv * a.g.page + pos % a.g.page;
     }
-    if (!placed) {
-      const int s = warp_segment(a.g.cu, (int)a.g.n_seqs, t);
-      if (s < 0) return;                                  // behind the last sequence
-      const int64_t c0 = __ldg(a.g.cu + s), c1 = __ldg(a.g.cu + s + 1);
-      const int64_t pos = (int64_t)__ldg(a.g.kv_lens + s) - (c1 - c0) + (t - c0);
-      if (pos >= 0 && pos < a.g.max_pages * a.g.page) {
-        const int64_t pg = __ldg(a.g.table + (int64_t)s * a.g.max_pages + pos / a.g.page);
-        if (pg >= 0 && pg < a.g.n_pages)
-          slot = pg * a.hkv * a.g.page + pos % a.g.page;
-      }
-      if (slot < 0 && lane == 0) set_device_error(err, MSA_DEVERR_PAGE_RANGE);
-      if (a.rotate) {
-        lane_cos_sin<N>(a.tn, c, pos, cs, sn);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) { cs[e] = 1.f; sn[e] = 0.f; }
-      }
-      placed = true;
+    if (slot < 0 && lane == 0) set_device_error(err, MSA_DEVERR_PAGE_RANGE);
+  };
+  auto place = [&](float (&cs)[N], float (&sn)[N]) {
+    find();
+    if (!angles && a.rotate) {
+      lane_cos_sin<N, R::kLanes>(a.tn, pos, cs0, sn0);
+      angles = true;
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * a.split * R::kRows + sub;
-      float xa[N], xb[N];
-      const bool on = h < heads;
-      Vec16<T>::unpack(on ? ra[u] : make_uint4(0, 0, 0, 0), xa);
-      Vec16<T>::unpack(on ? rb[u] : make_uint4(0, 0, 0, 0), xb);
-      const float r = a.eps > 0.f ? row_rstd<D, N, R::kLanes>(xa, xb, a.eps) : 1.f;
-      if (!on || (h >= a.hq && slot < 0)) continue;
-      if (h >= hk) {                                      // values are copied
-        T* out = vp + (slot + (int64_t)(h - hk) * a.g.page) * D;
-        *reinterpret_cast<uint4*>(out + c * N) = ra[u];
-        *reinterpret_cast<uint4*>(out + D / 2 + c * N) = rb[u];
-        continue;
-      }
-      const T* w = h < a.hq ? wq : wk;
-      if (a.eps > 0.f) {
-        float wa[N], wb[N];
-        if (w != nullptr) {
-          Vec16<T>::unpack(ldg16(w + c * N), wa);
-          Vec16<T>::unpack(ldg16(w + D / 2 + c * N), wb);
-        } else {
-#pragma unroll
-          for (int e = 0; e < N; ++e) wa[e] = wb[e] = 1.f;
-        }
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          xa[e] = xa[e] * r * wa[e];
-          xb[e] = xb[e] * r * wb[e];
-        }
-      }
-      T* out = h < a.hq ? qo + (t * a.hq + h) * D : kp + (slot + (int64_t)(h - a.hq) * a.g.page) * D;
-      float ya[N], yb[N];
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        ya[e] = xa[e] * cs[e] - xb[e] * sn[e];
-        yb[e] = xb[e] * cs[e] + xa[e] * sn[e];
-      }
-      store_n<T>(out + c * N, ya);
-      store_n<T>(out + D / 2 + c * N, yb);
+    for (int e = 0; e < N; ++e) {
+      cs[e] = a.rotate ? cs0[e] : 1.f;
+      sn[e] = a.rotate ? sn0[e] : 0.f;
     }
+    return true;
+  };
+  turn_heads<T, D, kUnroll>(q + t * a.qs, qo + t * a.hq * D, D, a.hq, wq, a.eps, part, a.split, gq,
+                            [&](float (&cs)[N], float (&sn)[N]) {
+                              place(cs, sn);
+                              return mine;
+                            });
+  // (where the keys go is known only after find(): the rows are placed from the slot)
+  const int g0 = first_group(gq, part, a.split) - gq;
+  if (g0 < gk) {
+    find();
+    turn_heads<T, D, 2>(k + t * a.ks, kp + max(slot, (int64_t)0) * D, a.g.page * D, a.hkv, wk,
+                        a.eps, g0, a.split, gk, [&](float (&cs)[N], float (&sn)[N]) {
+                          place(cs, sn);
+                          return slot >= 0;
+                        });
+  }
+  // values are copied
+  for (int g = first_group(gq + gk, part, a.split) - gq - gk; g < gk; g += a.split) {
+    const int h = g * R::kRows + sub;
+    const T* row = v + t * a.vs + (int64_t)h * D;
+    uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
+    if (h < a.hkv) {
+      ra = ld16_once(row + c * N);
+      rb = ld16_once(row + D / 2 + c * N);
+    }
+    find();                                               // (all lanes)
+    if (slot < 0 || h >= a.hkv) continue;
+    T* out = vp + (slot + (int64_t)h * a.g.page) * D;
+    *reinterpret_cast<uint4*>(out + c * N) = ra;
+    *reinterpret_cast<uint4*>(out + D / 2 + c * N) = rb;
   }
 }
 
 template <typename T, int D>
 cudaError_t run(AppendArgs& a, const void* q, const void* k, const void* v, const void* wq,
                 const void* wk, void* kp, void* vp, void* qo, int* err, cudaStream_t st) {
-  const int rows = RowLayout<T, D>::kRows;
-  const int groups = (a.hq + 2 * a.hkv + rows - 1) / rows;
-  const int64_t want = (int64_t)sm_count() * 32;
-  a.split = 1;
-  while (a.split < groups && a.n_tok * a.split < want) a.split *= 2;
-  if (a.split > groups) a.split = groups;
+  constexpr int kR = RowLayout<T, D>::kRows;
+  a.split = head_split(a.n_tok, (a.hq + kR - 1) / kR + 2 * ((a.hkv + kR - 1) / kR));
   const int64_t grid = (a.n_tok * a.split + kWarps - 1) / kWarps;
   paged_append_kernel<T, D><<<(unsigned)grid, kWarps * 32, 0, st>>>(
       (const T*)q, (const T*)k, (const T*)v, (const T*)wq, (const T*)wk, (T*)kp, (T*)vp, (T*)qo,

@@ -93,8 +93,8 @@ cudaError_t run_combine(const PagedAttn& a, int grid, int rows, const PagedParts
 PagedParts parts_of(char* ws) {
   PagedParts p;
   p.rec = reinterpret_cast<int4*>(ws);
-  p.ml = reinterpret_cast<float2*>(ws + kPagedCtas * sizeof(int4));
-  p.o = reinterpret_cast<float*>(ws + kPagedCtas * sizeof(int4) +
+  p.ml = reinterpret_cast<float2*>(ws + kPagedRecs * sizeof(int4));
+  p.o = reinterpret_cast<float*>(ws + kPagedRecs * sizeof(int4) +
                                  (size_t)2 * kPagedCtas * kPagedMaxRows * sizeof(float2));
   return p;
 }
@@ -102,7 +102,7 @@ PagedParts parts_of(char* ws) {
 }  // namespace
 
 size_t paged_attn_ws_bytes(const HeadShape& s) {
-  return kPagedCtas * sizeof(int4) +
+  return kPagedRecs * sizeof(int4) +
          (size_t)2 * kPagedCtas * kPagedMaxRows * (sizeof(float2) + s.d * sizeof(float));
 }
 
@@ -147,7 +147,7 @@ cudaError_t launch_paged_attn(const HeadShape& s, const PagedShape& g, int64_t m
   const int64_t rows = max_new * a.G;
   const PagedParts parts = parts_of(ws);
   if (s.dtype == MSA_F32)
-    return launch_paged_simt(s, a, rows <= 16 ? 16 : 64, q, kp, vp, o, lse, parts, err, st);
+    return launch_paged_f32(s, a, rows <= 8 ? (int)rows : 64, q, kp, vp, o, lse, parts, err, st);
   if (rows <= 64 || scale < 0.f)       // (the chunk kernel takes maxima of unscaled scores)
     return launch_paged_few(s, a, rows <= 16 ? (int)rows : 64, q, kp, vp, o, lse, parts, err, st);
   return launch_paged_chunk(s, a, q, kp, vp, o, lse, parts, err, st);

@@ -12,8 +12,7 @@
 //                   thread run in order, so S_X of the next tile may be issued right behind the
 //                   product that reads P_X from the same columns;
 //   two warpgroups  the softmax of one half each, one thread a row: scores from TMEM, base-2
-//                   exponentials (part of them on the FMA pipe, fastmath.cuh), P back to TMEM as
-//                   bf16 (rounded once, 2^-9 of each weight).  The exponent reference moves only
+//                   exponentials, P back to TMEM as bf16 (rounded once, 2^-9 of each weight).  The exponent reference moves only
 //                   when a row's maximum outgrows it by 2^8, so O is rarely rescaled.  (The
 //                   maximum is that of the raw scores: the scale must not be negative.)
 // TMEM columns: S_0 / P_0 [0, 128), S_1 / P_1 [128, 256), O_0 [256, ..), O_1 [384, ..).
@@ -36,17 +35,7 @@ constexpr int kIssuer = 8, kProducer = 9;
 constexpr uint32_t kHalf = 128 * 128; // 128 rows x 64 dims
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.f;
-#ifndef POLY
-#define POLY quintic_exp2x2
-#endif
-#ifndef CHUNK_LEAD
-#define CHUNK_LEAD 3
-#endif
-#ifndef CHUNK_POLY
-#define CHUNK_POLY 0
-#endif
-constexpr int kLead = CHUNK_LEAD;
-constexpr int kPolyPairs = CHUNK_POLY;       // pairs of each 8 whose exponentials use the FMA pipe
+constexpr int kLead = 3;              // cost of an item beside its tiles, in tiles
 
 template <int D> constexpr uint32_t kUnit = KT * D * 2;      // one K or V tile
 template <int D> constexpr int kUnits = D == 128 ? 5 : 10;   // 160 KB
@@ -149,12 +138,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_t, uint32_t o_t, float c
     for (int k = 0; k < 32; k += 2) {
       float x0, x1, p0, p1;
       ffma2(x0, x1, __uint_as_float(sv[w][k]), __uint_as_float(sv[w][k + 1]), c2, c2, -mb, -mb);
-      if ((kPolyPairs >> ((k / 2) & 7)) & 1) {
-        POLY(x0, x1, p0, p1);
-      } else {
-        p0 = fast_exp2(x0);
-        p1 = fast_exp2(x1);
-      }
+      p0 = fast_exp2(x0);
+      p1 = fast_exp2(x1);
       if (!FULL) {
         p0 = w * 32 + k < lim ? p0 : 0.f;
         p1 = w * 32 + k + 1 < lim ? p1 : 0.f;

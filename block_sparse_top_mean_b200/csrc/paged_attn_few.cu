@@ -19,44 +19,22 @@
 //     would no longer hide).
 // Keys behind the last visible one are not loaded past their page piece; their scores are
 // replaced, and their V rows (which may hold anything) masked in the fragments.
-#include "paged.cuh"
+#include "paged_ring.cuh"
 #include "fastmath.cuh"
-#include "sm100.cuh"
 
 namespace msa {
 namespace {
 
-using namespace sm100;
+using namespace paged;
 using fastmath::fast_exp2;
 
-constexpr int KT = 32;                // keys of a tile
-#ifndef FEW_WARPS
-#define FEW_WARPS 4
-#endif
-constexpr int kConsumers = FEW_WARPS; // warps 0-3; warp 4 produces
+constexpr int kConsumers = 4;         // warps 0-3; warp 4 produces
 constexpr int kThreads = 32 * (kConsumers + 1);
+// What an item costs beside its tiles, in tiles (48 sequences of 1 to 16384 keys: 0 168 us, 4 71,
+// 7 61, 10 64).
+constexpr int kLead = 7;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr uint32_t kHalf = KT * 128;  // 32 keys x 64 dims
-#ifndef FEW_LEAD
-#define FEW_LEAD 7
-#endif
-constexpr int kLead = FEW_LEAD;
-#ifndef FEW_ST
-#define FEW_ST 12
-#endif
-template <int D> constexpr uint32_t kTileBytes = KT * D * 2;
-template <int D> constexpr uint32_t kStageBytes = 2 * kTileBytes<D>;
 
-// ST stages.  Where a tile belongs to one warp, ST is a multiple of the warps, so that a stage
-// always belongs to the same warp: a parity wait tells a phase only from its neighbours, and a
-// warp that took over another's stage could be a whole round ahead of a copy that is late.
-template <int D, int ST>
-struct __align__(16) Ring {
-  static_assert(ST % kConsumers == 0, "a stage keeps its warp");
-  uint64_t full[ST], empty[ST];
-  int abort;
-  PlanSmem plan;
-};
 // The warps' outputs of an item, joined when it ends.
 template <int D, int R>
 struct __align__(16) Join {
@@ -86,7 +64,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 // Byte offset of 16-byte chunk c (8 dims each) of key row r inside a K or V tile.
 __device__ __forceinline__ uint32_t tile_off(int r, int c) {
-  return (uint32_t)(c >> 3) * kHalf + (uint32_t)r * 128u + ((uint32_t)((c & 7) ^ (r & 7)) << 4);
+  return (uint32_t)(c >> 3) * kSlice + (uint32_t)r * 128u + ((uint32_t)((c & 7) ^ (r & 7)) << 4);
 }
 // Clears the bf16 lanes of a fragment word whose keys (k, k + 1) are not below lim.
 __device__ __forceinline__ uint32_t keep_keys(uint32_t w, int k, int lim) {
@@ -94,103 +72,6 @@ __device__ __forceinline__ uint32_t keep_keys(uint32_t w, int k, int lim) {
 }
 __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
-}
-
-template <int D, int ST>
-__device__ __forceinline__ void ring_fail(Ring<D, ST>& sm, int* err) {
-  set_device_error(err, MSA_DEVERR_TIMEOUT);
-  *(volatile int*)&sm.abort = 1;
-}
-
-// Waits for a phase of one of the ring's barriers, for the whole warp; false when the wait ran
-// out (after ~2 s) or another warp's did.
-template <int D, int ST>
-__device__ __forceinline__ bool ring_wait(Ring<D, ST>& sm, uint64_t* bar, uint32_t parity, int* err) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  const long long t0 = clock64();
-  while (!ok && *(volatile int*)&sm.abort == 0 && clock64() - t0 < 4000000000LL)
-    ok = mbar_try_wait(bar, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  if (threadIdx.x % 32 == 0) ring_fail(sm, err);
-  return false;
-}
-
-// The producer warp: copies every tile of the run, in order.
-template <int D, int ST>
-__device__ __forceinline__ void produce(const CUtensorMap& tm_k, const CUtensorMap& tm_v, int box,
-                                        unsigned char* ring, Ring<D, ST>& sm, Run r, int* err,
-                                        const PagedAttn& a) {
-  const int lane = threadIdx.x % 32;
-  const int per = KT / box;                               // page pieces of a tile
-  const int rows = (int)(a.g.n_pages * a.hkv * a.g.page);
-  int step = 0, st = 0;                                   // copies so far; the next one's stage
-  uint32_t ph = 1;                                        // of the stage's empty barrier
-  bool ok = true;
-  do {
-    const int tile0 = run_first(a, r), nt = run_tiles(a, r), vis = tile_keys(a, r.v, r.rt);
-    if (nt == 0) break;                                   // the run ends in the item's lead
-    // row of piece i of the item's part of this run in the pools, `rows` (reads as zeros)
-    // for an entry that is no page, -1 past the last visible key
-    auto piece_row = [&](int i) -> int {
-      const int key = tile0 * KT + i * box;
-      if (i >= nt * per || key >= vis) return -1;
-      const int pg = key_page(a, r.s, key, err);
-      return pg < 0 ? rows : (int)(((int64_t)pg * a.hkv + r.g) * a.g.page + key % (int)a.g.page);
-    };
-    int cur = piece_row(lane), nxt = piece_row(32 + lane);
-    for (int it = 0; it < nt; ++it, ++step) {
-      const int at = it * per;                            // first piece of the tile
-      if (at > 0 && at % 32 == 0) {
-        cur = nxt;
-        nxt = piece_row(at + 32 + lane);
-      }
-      // (the first pass over the ring waits for the phase before the first: it is over)
-      if (!ring_wait(sm, &sm.empty[st], ph, err)) {
-        ok = false;
-        break;
-      }
-      const int y = __shfl_sync(0xffffffffu, cur, (at & 31) + (lane < per ? lane : 0));
-      const bool mine = lane < per && y >= 0;
-      const int n = __popc(__ballot_sync(0xffffffffu, mine));
-      if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], (uint32_t)(n * box * D * 4));
-      __syncwarp();
-      if (mine) {
-        unsigned char* dst = ring + st * kStageBytes<D> + lane * box * 128;
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          tma_load_2d(dst + h * kHalf, &tm_k, &sm.full[st], h * 64, y);
-          tma_load_2d(dst + kTileBytes<D> + h * kHalf, &tm_v, &sm.full[st], h * 64, y);
-        }
-      }
-      if (++st == ST) {
-        st = 0;
-        ph ^= 1;
-      }
-    }
-  } while (ok && run_next<KT>(a, r));
-  if (!ok)                                                // no copy may land after the CTA ends
-    for (int s = step > ST ? step - ST : 0; s < step; ++s)
-      mbar_wait_warp(&sm.full[s % ST], (uint32_t)(s / ST) & 1);
-}
-
-// Set-up shared by both kernels: barriers, this CTA's record, the run.
-template <int D, int ST>
-__device__ __forceinline__ Run begin(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                     Ring<D, ST>& sm, int readers, const PagedParts& parts,
-                                     const PagedAttn& a) {
-  if (threadIdx.x == 0) {
-    prefetch_tmap(&tm_k);
-    prefetch_tmap(&tm_v);
-    for (int s = 0; s < ST; ++s) {
-      mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], readers);
-    }
-    sm.abort = 0;
-    fence_mbar_init();
-    parts.rec[blockIdx.x] = make_int4(0, 0, 0, 0);
-  }
-  return paged_plan<KT, kThreads>(a, &sm.plan);           // synchronises the CTA
 }
 
 // ------------------------------------------------------------------ up to 8 * NQ rows
@@ -211,13 +92,13 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* ring = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Ring<D, ST>& sm = *reinterpret_cast<Ring<D, ST>*>(ring + ST * kStageBytes<D>);
-  Join<D, R>& jn = *reinterpret_cast<Join<D, R>*>(ring + ST * kStageBytes<D> + sizeof(Ring<D, ST>));
+  Ring<ST, kConsumers>& sm = *reinterpret_cast<Ring<ST, kConsumers>*>(ring + ST * kStageBytes<D, 2>);
+  Join<D, R>& jn = *reinterpret_cast<Join<D, R>*>(ring + ST * kStageBytes<D, 2> + sizeof(Ring<ST, kConsumers>));
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  Run r = begin(tm_k, tm_v, sm, 1, parts, a);
+  Run r = begin<kThreads>(tm_k, tm_v, sm, 1, parts, a);
   if (r.at >= r.end) return;
   if (warp == kConsumers) {
-    produce(tm_k, tm_v, box, ring, sm, r, err, a);
+    produce<D, 2>(tm_k, tm_v, box, ring, sm, r, err, a);
     return;
   }
   // thread (gr, t4) of a warp: scores of keys gr, gr + 8 of a 16-key block and queries 2 t4,
@@ -280,7 +161,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
         aborted = true;
         break;
       }
-      const uint32_t sk = smem_u32(ring + st * kStageBytes<D>), sv = sk + kTileBytes<D>;
+      const uint32_t sk = smem_u32(ring + st * kStageBytes<D, 2>), sv = sk + kTileBytes<D, 2>;
       const int key0 = (tile0 + it) * KT;
       float s[NQ][2][4];
 #pragma unroll
@@ -294,7 +175,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
           uint32_t f[4];
-          ldsm4(sk + k_off[ks & 3] + (ks >> 2) * kHalf + kb * 2048, f);
+          ldsm4(sk + k_off[ks & 3] + (ks >> 2) * kSlice + kb * 2048, f);
 #pragma unroll
           for (int n = 0; n < NQ; ++n) mma16816(s[n][kb], f, qb[n][ks][0], qb[n][ks][1]);
         }
@@ -359,7 +240,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt) {
           uint32_t f[4];                                  // (dims, keys): (0,0) (8,0) (0,8) (8,8)
-          ldsm4_t(sv + v_off[dt & 3] + (dt >> 2) * kHalf + kb * 2048, f);
+          ldsm4_t(sv + v_off[dt & 3] + (dt >> 2) * kSlice + kb * 2048, f);
           if (lim < KT) {
 #pragma unroll
             for (int w = 0; w < 4; ++w) f[w] = keep_keys(f[w], kb * 16 + (w >> 1) * 8 + 2 * t4, lim);
@@ -446,12 +327,12 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k,
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* ring = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Ring<D, ST>& sm = *reinterpret_cast<Ring<D, ST>*>(ring + ST * kStageBytes<D>);
+  Ring<ST, kConsumers>& sm = *reinterpret_cast<Ring<ST, kConsumers>*>(ring + ST * kStageBytes<D, 2>);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  Run r = begin(tm_k, tm_v, sm, kConsumers, parts, a);
+  Run r = begin<kThreads>(tm_k, tm_v, sm, kConsumers, parts, a);
   if (r.at >= r.end) return;
   if (warp == kConsumers) {
-    produce(tm_k, tm_v, box, ring, sm, r, err, a);
+    produce<D, 2>(tm_k, tm_v, box, ring, sm, r, err, a);
     return;
   }
   const int gr = lane >> 2, t4 = lane & 3, mi = lane >> 3, ri = lane & 7;
@@ -491,7 +372,7 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k,
         aborted = true;
         break;
       }
-      const uint32_t sk = smem_u32(ring + st * kStageBytes<D>), sv = sk + kTileBytes<D>;
+      const uint32_t sk = smem_u32(ring + st * kStageBytes<D, 2>), sv = sk + kTileBytes<D, 2>;
       const int key0 = (tile0 + it) * KT;
       float s[KT / 8][4];
 #pragma unroll
@@ -613,20 +494,15 @@ paged_few_kernel(const __grid_constant__ CUtensorMap tm_k,
   } while (run_next<KT>(a, r));
 }
 
-template <int D, int ST>
-constexpr size_t ring_bytes() { return 1024 + ST * kStageBytes<D> + sizeof(Ring<D, ST>); }
-
 template <typename K>
 cudaError_t run(K kernel, std::atomic<uint64_t>* done, int rows, size_t smem, PagedAttn& a, const HeadShape& s, const void* q,
                 const void* kp, const void* vp, void* o, float* lse, const PagedParts& parts,
                 int* err, cudaStream_t st) {
   a.tt = rows / a.G;
   a.lead = kLead;
-  const int box = a.g.page % 32 == 0 ? 32 : 16;           // keys of one copy: they share a page
-  const int64_t pool = a.g.n_pages * a.hkv * a.g.page;
+  int box = 0;
   CUtensorMap mk{}, mv{};
-  if (!make_bf16_2d_map(&mk, kp, pool, s.d, box) || !make_bf16_2d_map(&mv, vp, pool, s.d, box))
-    return cudaErrorInvalidValue;
+  if (!pool_maps(a, s, kp, vp, &mk, &mv, &box)) return cudaErrorInvalidValue;
   cudaError_t e = raise_smem((const void*)kernel, smem, done);
   if (e != cudaSuccess) return e;
   const int grid = paged_grid();
@@ -640,17 +516,17 @@ template <int D>
 cudaError_t run_rows(int rows, PagedAttn& a, const HeadShape& s, const void* q, const void* kp,
                      const void* vp, void* o, float* lse, const PagedParts& parts, int* err,
                      cudaStream_t st) {
-  constexpr int ST = FEW_ST * 128 / D;                    // 192 KB of tiles
+  constexpr int ST = 12 * 128 / D;                    // 192 KB of tiles
   static std::atomic<uint64_t> done[3];
   if (rows <= 8)
-    return run(paged_step_kernel<D, 1, ST>, &done[0], 8, ring_bytes<D, ST>() + sizeof(Join<D, 8>), a, s, q,
+    return run(paged_step_kernel<D, 1, ST>, &done[0], 8, ring_bytes<D, 2, ST, kConsumers>() + sizeof(Join<D, 8>), a, s, q,
                kp, vp, o, lse, parts, err, st);
   if (rows <= 16) {
     constexpr int ST2 = D == 128 ? 8 : ST;                // room for 16 rows of four warps
-    return run(paged_step_kernel<D, 2, ST2>, &done[1], 16, ring_bytes<D, ST2>() + sizeof(Join<D, 16>), a, s,
+    return run(paged_step_kernel<D, 2, ST2>, &done[1], 16, ring_bytes<D, 2, ST2, kConsumers>() + sizeof(Join<D, 16>), a, s,
                q, kp, vp, o, lse, parts, err, st);
   }
-  return run(paged_few_kernel<D, ST>, &done[2], 64, ring_bytes<D, ST>(), a, s, q, kp, vp, o, lse, parts, err,
+  return run(paged_few_kernel<D, ST>, &done[2], 64, ring_bytes<D, 2, ST, kConsumers>(), a, s, q, kp, vp, o, lse, parts, err,
              st);
 }
 

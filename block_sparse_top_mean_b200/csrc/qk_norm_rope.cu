@@ -35,7 +35,8 @@ Turns make_turns(double base, int d) {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kUnroll = 4;            // rows in flight per lane
+constexpr int kUnroll = 4;            // row groups in flight per warp
+constexpr int kBwdCtas = 2;           // of the backward kernel on an SM
 
 struct NormArgs {
   Turns tn;
@@ -51,212 +52,178 @@ __device__ __forceinline__ int64_t token_pos(const int32_t* cu, int n_docs, int6
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 2)
 qk_norm_rope_kernel(const T* q, const T* k, const int32_t* __restrict__ cu,
                     const T* __restrict__ wq, const T* __restrict__ wk, T* qo, T* ko,
                     const __grid_constant__ NormArgs a) {
   using R = RowLayout<T, D>;
   constexpr int N = R::N;
-  const int lane = threadIdx.x & 31, c = lane % R::kLanes, sub = lane / R::kLanes;
   const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t t = unit / a.split;
   if (t >= a.n_tok) return;                               // whole warp
   const int part = (int)(unit - t * a.split);
-  const int heads = a.hq + a.hkv;
-  const T* qt = q + t * a.qs;
-  const T* kt = k + t * a.ks;
-  float cs[N], sn[N];
+  const int gq = (a.hq + R::kRows - 1) / R::kRows, gk = (a.hkv + R::kRows - 1) / R::kRows;
+  float cs0[N], sn0[N];
   bool placed = false;
-  for (int h0 = part * R::kRows; h0 < heads; h0 += a.split * R::kRows * kUnroll) {
-    uint4 ra[kUnroll], rb[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * a.split * R::kRows + sub;
-      if (h >= heads) continue;
-      const T* row = h < a.hq ? qt + (int64_t)h * D : kt + (int64_t)(h - a.hq) * D;
-      ra[u] = ld16_once(row + c * N);
-      rb[u] = ld16_once(row + D / 2 + c * N);
-    }
+  auto place = [&](float (&cs)[N], float (&sn)[N]) {
     if (!placed) {
-      lane_cos_sin<N>(a.tn, c, token_pos(cu, a.n_docs, t), cs, sn);
+      lane_cos_sin<N, R::kLanes>(a.tn, token_pos(cu, a.n_docs, t), cs0, sn0);
       placed = true;
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * a.split * R::kRows + sub;
-      float xa[N], xb[N], wa[N], wb[N];
-      const bool on = h < heads;
-      Vec16<T>::unpack(on ? ra[u] : make_uint4(0, 0, 0, 0), xa);
-      Vec16<T>::unpack(on ? rb[u] : make_uint4(0, 0, 0, 0), xb);
-      const float r = row_rstd<D, N, R::kLanes>(xa, xb, a.eps);
-      if (!on) continue;
-      const T* w = h < a.hq ? wq : wk;
-      if (w != nullptr) {
-        Vec16<T>::unpack(ldg16(w + c * N), wa);
-        Vec16<T>::unpack(ldg16(w + D / 2 + c * N), wb);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) wa[e] = wb[e] = 1.f;
-      }
-      T* out = h < a.hq ? qo + (t * a.hq + h) * D : ko + (t * a.hkv + (h - a.hq)) * D;
-      float ya[N], yb[N];
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float na = xa[e] * r * wa[e], nb = xb[e] * r * wb[e];
-        ya[e] = na * cs[e] - nb * sn[e];
-        yb[e] = nb * cs[e] + na * sn[e];
-      }
-      store_n<T>(out + c * N, ya);
-      store_n<T>(out + D / 2 + c * N, yb);
-    }
-  }
+    for (int e = 0; e < N; ++e) { cs[e] = cs0[e]; sn[e] = sn0[e]; }
+    return true;
+  };
+  turn_heads<T, D, kUnroll>(q + t * a.qs, qo + t * a.hq * D, D, a.hq, wq, a.eps, part, a.split, gq,
+                            place);
+  turn_heads<T, D, 2>(k + t * a.ks, ko + t * a.hkv * D, D, a.hkv, wk, a.eps,
+                      first_group(gq, part, a.split) - gq, a.split, gk, place);
 }
 
 // ------------------------------------------------------------------ backward
-// Persistent warps, one token each at a time.  part[cta][2][D]: the CTA's sums for wq, wk.
+// CTAs below nq take the queries, the others the keys (so a lane keeps one set of sums and
+// enough warps fit); persistent warps, one token (or part of its heads) each at a time.
+// part[cta][D]: the CTA's sums.
+struct BwdArgs {
+  NormArgs n;
+  int nq, split_k;                    // n.split: of the queries
+};
+
 template <typename T, typename TG, int D>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, kBwdCtas)
 qk_norm_rope_bwd_kernel(const TG* __restrict__ dq, const TG* __restrict__ dk,
                         const T* __restrict__ q, const T* __restrict__ k,
                         const int32_t* __restrict__ cu, const T* __restrict__ wq,
                         const T* __restrict__ wk, T* __restrict__ dqi, T* __restrict__ dki,
-                        float* __restrict__ part, const __grid_constant__ NormArgs a) {
+                        float* __restrict__ part, const __grid_constant__ BwdArgs b) {
   using R = RowLayout<T, D>;
   constexpr int N = R::N;
-  __shared__ float s_dw[kWarps][2][D];
+  __shared__ float s_dw[kWarps][D];
+  const NormArgs& a = b.n;
   const int lane = threadIdx.x & 31, c = lane % R::kLanes, sub = lane / R::kLanes;
   const int warp = threadIdx.x >> 5;
-  float acc[2][2][N];                                     // [q, k][half][pair]
+  const bool keys = (int)blockIdx.x >= b.nq;
+  const int cta = keys ? blockIdx.x - b.nq : blockIdx.x;
+  const int n_cta = keys ? gridDim.x - b.nq : b.nq;
+  const int heads = keys ? a.hkv : a.hq, split = keys ? b.split_k : a.split;
+  const int64_t stride = keys ? a.ks : a.qs;
+  const T* x0 = keys ? k : q;
+  const TG* y0 = keys ? dk : dq;
+  T* o0 = keys ? dki : dqi;
+  const int groups = (heads + R::kRows - 1) / R::kRows;
+  float wa[N], wb[N], acc_a[N], acc_b[N];
+  load_weights<T, D>(keys ? wk : wq, c, wa, wb);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int e = 0; e < N; ++e) acc[i][0][e] = acc[i][1][e] = 0.f;
+  for (int e = 0; e < N; ++e) acc_a[e] = acc_b[e] = 0.f;
 
-  const int64_t units = a.n_tok * a.split;
-  for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < units;
-       unit += (int64_t)gridDim.x * kWarps) {
-    const int64_t t = unit / a.split;
-    const int part_i = (int)(unit - t * a.split);
+  const int64_t units = a.n_tok * split;
+  for (int64_t unit = (int64_t)cta * kWarps + warp; unit < units;
+       unit += (int64_t)n_cta * kWarps) {
+    const int64_t t = unit / split;
+    const T* xt = x0 + t * stride + c * N;
+    const TG* gt = y0 + t * heads * D + c * N;
+    T* ot = o0 + t * heads * D + c * N;
     float cs[N], sn[N];
-    lane_cos_sin<N>(a.tn, c, token_pos(cu, a.n_docs, t), cs, sn);
+    lane_cos_sin<N, R::kLanes>(a.tn, token_pos(cu, a.n_docs, t), cs, sn);
+    float ta[N], tb[N];                                   // this token's heads
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {                         // queries, then keys
-      const int heads = i ? a.hkv : a.hq;
-      const T* xt = i ? k + t * a.ks : q + t * a.qs;
-      const TG* gt = (i ? dk : dq) + t * heads * D;
-      T* ot = (i ? dki : dqi) + t * heads * D;
-      const T* w = i ? wk : wq;
-      float wa[N], wb[N];
-      if (w != nullptr) {
-        Vec16<T>::unpack(ldg16(w + c * N), wa);
-        Vec16<T>::unpack(ldg16(w + D / 2 + c * N), wb);
+    for (int e = 0; e < N; ++e) ta[e] = tb[e] = 0.f;
+    for (int g = (int)(unit - t * split); g < groups; g += split) {
+      const int h = g * R::kRows + sub;
+      const bool on = h < heads;
+      float xa[N], xb[N], ga[N], gb[N];
+      if (on) {
+        load_n<T, N>(xt + h * D, xa);
+        load_n<T, N>(xt + h * D + D / 2, xb);
+        load_n<TG, N>(gt + h * D, ga);
+        load_n<TG, N>(gt + h * D + D / 2, gb);
       } else {
 #pragma unroll
-        for (int e = 0; e < N; ++e) wa[e] = wb[e] = 1.f;
+        for (int e = 0; e < N; ++e) xa[e] = xb[e] = ga[e] = gb[e] = 0.f;
       }
-      float ta[N], tb[N];                                 // this token's heads
-#pragma unroll
-      for (int e = 0; e < N; ++e) ta[e] = tb[e] = 0.f;
-#pragma unroll 2
-      for (int h0 = part_i * R::kRows; h0 < heads; h0 += a.split * R::kRows) {
-        const int h = h0 + sub;
-        const bool on = h < heads;
-        float xa[N], xb[N], ga[N], gb[N];
-        if (on) {
-          load_n<T, N>(xt + (int64_t)h * D + c * N, xa);
-          load_n<T, N>(xt + (int64_t)h * D + D / 2 + c * N, xb);
-          load_n<TG, N>(gt + (int64_t)h * D + c * N, ga);
-          load_n<TG, N>(gt + (int64_t)h * D + D / 2 + c * N, gb);
-        } else {
-#pragma unroll
-          for (int e = 0; e < N; ++e) xa[e] = xb[e] = ga[e] = gb[e] = 0.f;
-        }
-        const float r = row_rstd<D, N, R::kLanes>(xa, xb, a.eps);
-        float dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float y0 = ga[e], y1 = gb[e];
-          xa[e] *= r;
-          xb[e] *= r;
-          const float g0 = y0 * cs[e] + y1 * sn[e], g1 = y1 * cs[e] - y0 * sn[e];
-          ta[e] = fmaf(g0, xa[e], ta[e]);
-          tb[e] = fmaf(g1, xb[e], tb[e]);
-          ga[e] = g0 * wa[e];
-          gb[e] = g1 * wb[e];
-          dot = fmaf(ga[e], xa[e], fmaf(gb[e], xb[e], dot));
-        }
-        dot = row_sum<R::kLanes>(dot) * (1.f / D);
-        if (!on) continue;
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          ga[e] = r * fmaf(-xa[e], dot, ga[e]);
-          gb[e] = r * fmaf(-xb[e], dot, gb[e]);
-        }
-        store_n<T>(ot + (int64_t)h * D + c * N, ga);
-        store_n<T>(ot + (int64_t)h * D + D / 2 + c * N, gb);
-      }
+      const float r = row_rstd<D, N, R::kLanes>(xa, xb, a.eps);
+      float d0 = 0.f, d1 = 0.f;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        acc[i][0][e] += ta[e];
-        acc[i][1][e] += tb[e];
+        const float g0 = fmaf(ga[e], cs[e], gb[e] * sn[e]);       // R^T dy of both halves
+        const float g1 = fmaf(gb[e], cs[e], -(ga[e] * sn[e]));
+        xa[e] *= r;
+        xb[e] *= r;
+        ta[e] = fmaf(g0, xa[e], ta[e]);
+        tb[e] = fmaf(g1, xb[e], tb[e]);
+        ga[e] = g0 * wa[e];
+        gb[e] = g1 * wb[e];
+        d0 = fmaf(ga[e], xa[e], d0);
+        d1 = fmaf(gb[e], xb[e], d1);
       }
+      const float dot = row_sum<R::kLanes>(d0 + d1) * (-1.f / D);
+      if (!on) continue;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        ga[e] = r * fmaf(xa[e], dot, ga[e]);
+        gb[e] = r * fmaf(xb[e], dot, gb[e]);
+      }
+      store_n<T>(ot + h * D, ga);
+      store_n<T>(ot + h * D + D / 2, gb);
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      acc_a[e] += ta[e];
+      acc_b[e] += tb[e];
     }
   }
   if (part == nullptr) return;
   // rows of the warp (lanes with the same c), then the warps of the CTA in order
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int e = 0; e < N; ++e) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        float x = acc[i][h][e];
-#pragma unroll
-        for (int o = 16; o >= R::kLanes; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (sub == 0) s_dw[warp][i][h * (D / 2) + c * N + e] = x;
-      }
+    for (int o = 16; o >= R::kLanes; o >>= 1) {
+      acc_a[e] += __shfl_xor_sync(0xffffffffu, acc_a[e], o);
+      acc_b[e] += __shfl_xor_sync(0xffffffffu, acc_b[e], o);
+    }
+    if (sub == 0) {
+      s_dw[warp][c * N + e] = acc_a[e];
+      s_dw[warp][D / 2 + c * N + e] = acc_b[e];
+    }
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
+  for (int i = threadIdx.x; i < D; i += kWarps * 32) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += (&s_dw[w][0][0])[i];
-    part[(int64_t)blockIdx.x * 2 * D + i] = s;
+    for (int w = 0; w < kWarps; ++w) s += s_dw[w][i];
+    part[(int64_t)blockIdx.x * D + i] = s;
   }
 }
 
-// dw[i] = sum over CTAs of part[cta][i]: 32 columns a block, 32 slices of the CTAs.
+// dw[i] = sum over CTAs of part[cta][i]: 32 columns a block, 32 slices of the CTAs.  Blocks below
+// d / 32 sum the first nq CTAs (the queries'), the others the rest.
 __global__ void __launch_bounds__(1024)
-dw_sum_kernel(const float* __restrict__ part, int n_cta, int d, float* __restrict__ dwq,
+dw_sum_kernel(const float* __restrict__ part, int nq, int n_cta, int d, float* __restrict__ dwq,
               float* __restrict__ dwk) {
   __shared__ float s[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // launched beside the kernel above
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + x;
+  const bool keys = (int)blockIdx.x >= d / 32;
+  const int col = (blockIdx.x - (keys ? d / 32 : 0)) * 32 + x;
   float v = 0.f;
-  for (int c = y; c < n_cta; c += 32) v += part[(int64_t)c * 2 * d + col];
+  const int end = keys ? n_cta : nq;
+#pragma unroll 4
+  for (int c = (keys ? nq : 0) + y; c < end; c += 32) v += part[(int64_t)c * d + col];
   s[y][x] = v;
   __syncthreads();
   if (y != 0) return;
   v = 0.f;
 #pragma unroll
   for (int i = 0; i < 32; ++i) v += s[i][x];
-  float* dst = col < d ? dwq : dwk;
-  if (dst != nullptr) dst[col < d ? col : col - d] = v;
-}
-
-// Warps a token's heads are dealt to: one, unless the tokens alone leave the SMs without
-// enough warps; never more than there are row groups.
-int head_split(int64_t n_tok, int heads, int rows) {
-  const int64_t want = (int64_t)sm_count() * 32;
-  const int groups = (heads + rows - 1) / rows;
-  int s = 1;
-  while (s < groups && n_tok * s < want) s *= 2;
-  return s < groups ? s : groups;
+  float* dst = keys ? dwk : dwq;
+  if (dst != nullptr) dst[col] = v;
 }
 
 template <typename T, int D>
 cudaError_t run_fwd(NormArgs& a, const void* q, const void* k, const int32_t* cu, const void* wq,
                     const void* wk, void* qo, void* ko, cudaStream_t st) {
-  a.split = head_split(a.n_tok, a.hq + a.hkv, RowLayout<T, D>::kRows);
+  constexpr int kR = RowLayout<T, D>::kRows;
+  a.split = head_split(a.n_tok, (a.hq + kR - 1) / kR + (a.hkv + kR - 1) / kR);
   const int64_t grid = (a.n_tok * a.split + kWarps - 1) / kWarps;
   qk_norm_rope_kernel<T, D><<<(unsigned)grid, kWarps * 32, 0, st>>>(
       (const T*)q, (const T*)k, cu, (const T*)wq, (const T*)wk, (T*)qo, (T*)ko, a);
@@ -267,18 +234,39 @@ template <typename T, typename TG, int D>
 cudaError_t run_bwd(NormArgs& a, const void* dq, const void* dk, const void* q, const void* k,
                     const int32_t* cu, const void* wq, const void* wk, void* dqi, void* dki,
                     float* dwq, float* dwk, float* part, cudaStream_t st) {
-  a.split = head_split(a.n_tok, a.hq, RowLayout<T, D>::kRows);
-  int64_t grid = (a.n_tok * a.split + kWarps - 1) / kWarps;
+  constexpr int kR = RowLayout<T, D>::kRows;
+  BwdArgs b{};
+  a.split = head_split(a.n_tok, (a.hq + kR - 1) / kR);
+  b.split_k = head_split(a.n_tok, (a.hkv + kR - 1) / kR);
+  // The CTAs that fit the GPU, dealt out by row groups plus one for a token's position and
+  // angles (32768 tokens of 32 / 8 heads: 234 us; by rows alone 258); fewer where there is less
+  // work.
   const int64_t cap = qk_norm_rope_bwd_ctas();
-  if (grid > cap) grid = cap;
+  const int64_t want_q = (a.n_tok * a.split + kWarps - 1) / kWarps;
+  const int64_t want_k = (a.n_tok * b.split_k + kWarps - 1) / kWarps;
+  const int gq = (a.hq + kR - 1) / kR + 1, gk = (a.hkv + kR - 1) / kR + 1;
+  int64_t cap_q = cap * gq / (gq + gk);
+  if (cap_q > cap - 1) cap_q = cap - 1;
+  b.nq = (int)(want_q < cap_q ? want_q : cap_q);
+  const int64_t nk = want_k < cap - cap_q ? want_k : cap - cap_q;
+  b.n = a;
   const bool dw = dwq != nullptr || dwk != nullptr;
-  qk_norm_rope_bwd_kernel<T, TG, D><<<(unsigned)grid, kWarps * 32, 0, st>>>(
+  const int grid = b.nq + (int)nk;
+  qk_norm_rope_bwd_kernel<T, TG, D><<<grid, kWarps * 32, 0, st>>>(
       (const TG*)dq, (const TG*)dk, (const T*)q, (const T*)k, cu, (const T*)wq, (const T*)wk,
-      (T*)dqi, (T*)dki, dw ? part : nullptr, a);
+      (T*)dqi, (T*)dki, dw ? part : nullptr, b);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !dw) return e;
-  dw_sum_kernel<<<2 * D / 32, 1024, 0, st>>>(part, (int)grid, D, dwq, dwk);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = 2 * D / 32;
+  cfg.blockDim = 1024;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, dw_sum_kernel, (const float*)part, b.nq, grid, D, dwq, dwk);
 }
 
 NormArgs make_args(const HeadShape& s, int64_t n_docs, int64_t qs, int64_t ks, double base,
@@ -297,7 +285,7 @@ NormArgs make_args(const HeadShape& s, int64_t n_docs, int64_t qs, int64_t ks, d
 
 }  // namespace
 
-int64_t qk_norm_rope_bwd_ctas() { return 148 * 4; }
+int64_t qk_norm_rope_bwd_ctas() { return 148 * kBwdCtas; }
 
 cudaError_t launch_qk_norm_rope(const HeadShape& s, const int32_t* cu, int64_t n_docs,
                                 const void* q, int64_t qs, const void* k, int64_t ks,

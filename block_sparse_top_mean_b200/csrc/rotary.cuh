@@ -13,6 +13,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "fastmath.cuh"
 
 namespace msa {
 
@@ -51,22 +52,36 @@ __device__ __forceinline__ int warp_segment(const int32_t* __restrict__ cu, int 
   return lo;
 }
 
-// cos and sin of this lane's N pairs (pairs c*N .. c*N + N-1 of the head) at position pos.
-template <int N>
-__device__ __forceinline__ void lane_cos_sin(const Turns& tn, int c, int64_t pos, float* cs,
-                                             float* sn) {
-  const double p = (double)pos;
+// cos and sin of pair i of a head at position p.
+__device__ __forceinline__ void pair_cos_sin(double per_pos, double p, float& c, float& s) {
+  const double t = p * per_pos;
+  const double n4 = rint(4.0 * t);
+  const float r = (float)fma(-0.25, n4, t);
+  float s0, c0;
+  sincospif(2.f * r, &s0, &c0);
+  const int quad = (int)((long long)n4 & 3);
+  const float a = (quad & 1) ? s0 : c0, b = (quad & 1) ? c0 : s0;
+  c = (quad == 1 || quad == 2) ? -a : a;
+  s = (quad >= 2) ? -b : b;
+}
+
+// cos and sin of this lane's N pairs (pairs c*N .. c*N + N-1 of the head) at position pos.  The
+// kRows lanes that hold the same pairs form N / kRows of them each and pass them round: the
+// angles of a token cost the warp N / kRows evaluations, not N.
+template <int N, int kLanes>
+__device__ __forceinline__ void lane_cos_sin(const Turns& tn, int64_t pos, float (&cs)[N],
+                                             float (&sn)[N]) {
+  constexpr int kRows = 32 / kLanes, M = N / kRows;
+  static_assert(M >= 1 && M * kRows == N, "every lane forms the same number of pairs");
+  const int lane = threadIdx.x & 31, c = lane % kLanes, sub = lane / kLanes;
+  float co[M], si[M];
+#pragma unroll
+  for (int e = 0; e < M; ++e)
+    pair_cos_sin(tn.per_pos[c * N + sub * M + e], (double)pos, co[e], si[e]);
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    const double t = p * tn.per_pos[c * N + e];
-    const double n4 = rint(4.0 * t);
-    const float r = (float)fma(-0.25, n4, t);
-    float s, co;
-    sincospif(2.f * r, &s, &co);
-    const int quad = (int)((long long)n4 & 3);
-    const float a = (quad & 1) ? s : co, b = (quad & 1) ? co : s;
-    cs[e] = (quad == 1 || quad == 2) ? -a : a;
-    sn[e] = (quad >= 2) ? -b : b;
+    cs[e] = __shfl_sync(0xffffffffu, co[e % M], (e / M) * kLanes + c);
+    sn[e] = __shfl_sync(0xffffffffu, si[e % M], (e / M) * kLanes + c);
   }
 }
 
@@ -81,10 +96,26 @@ __device__ __forceinline__ float row_sum(float x) {
 // 1 / sqrt(mean(x^2) + eps) of the row held as (xa, xb) by its lanes.
 template <int D, int N, int kLanes>
 __device__ __forceinline__ float row_rstd(const float* xa, const float* xb, float eps) {
-  float s = 0.f;
+  float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-  for (int e = 0; e < N; ++e) s = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], s));
-  return __frsqrt_rn(fmaf(row_sum<kLanes>(s), 1.f / D, eps));
+  for (int e = 0; e < N; e += 2) {
+    fastmath::ffma2(s0, s1, xa[e], xa[e + 1], xa[e], xa[e + 1], s0, s1);
+    fastmath::ffma2(s0, s1, xb[e], xb[e + 1], xb[e], xb[e + 1], s0, s1);
+  }
+  return __frsqrt_rn(fmaf(row_sum<kLanes>(s0 + s1), 1.f / D, eps));
+}
+
+// Both halves of a lane's weights (ones where there are none).
+template <typename T, int D>
+__device__ __forceinline__ void load_weights(const T* w, int c, float* wa, float* wb) {
+  constexpr int N = Vec16<T>::N;
+  if (w != nullptr) {
+    Vec16<T>::unpack(ldg16(w + c * N), wa);
+    Vec16<T>::unpack(ldg16(w + D / 2 + c * N), wb);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) wa[e] = wb[e] = 1.f;
+  }
 }
 
 // 16-byte load of data read once.  Not the read-only path: a caller may rotate in place.
@@ -110,6 +141,83 @@ __device__ __forceinline__ void store_n(T* p, const float* f) {
 #pragma unroll
   for (int e = 0; e < N; ++e) y[e] = from_f32<T>(f[e]);
   *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(y);
+}
+
+// One token's heads of one tensor, normalised (eps > 0) and rotated: row groups g0, g0 + step, ..
+// below `groups` (kRows heads each) of src (heads D apart) to dst (heads `pitch` apart).  The
+// weights are folded into the rotation's factors, so an element costs three multiplications;
+// U groups' loads are issued before the first is used.  place() is called between the first
+// loads and their use: it finds the token's angles, and says whether to store.
+template <typename T, int D, int U, typename Place>
+__device__ __forceinline__ void turn_heads(const T* src, T* dst, int64_t pitch, int heads,
+                                           const T* w, float eps, int g0, int step, int groups,
+                                           Place place) {
+  using R = RowLayout<T, D>;
+  constexpr int N = R::N;
+  const int lane = threadIdx.x & 31, c = lane % R::kLanes, sub = lane / R::kLanes;
+  float ac[N], bs[N], bc[N], as[N];   // w_a cos, w_b sin, w_b cos, w_a sin
+  bool first = true, store = true;
+  for (int g = g0; g < groups; g += step * U) {
+    uint4 ra[U], rb[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = (g + u * step) * R::kRows + sub;
+      ra[u] = rb[u] = make_uint4(0, 0, 0, 0);
+      if (h < heads) {
+        ra[u] = ld16_once(src + (int64_t)h * D + c * N);
+        rb[u] = ld16_once(src + (int64_t)h * D + D / 2 + c * N);
+      }
+    }
+    if (first) {
+      float cs[N], sn[N], wa[N], wb[N];
+      load_weights<T, D>(w, c, wa, wb);
+      store = place(cs, sn);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        ac[e] = wa[e] * cs[e];
+        bs[e] = -wb[e] * sn[e];
+        bc[e] = wb[e] * cs[e];
+        as[e] = wa[e] * sn[e];
+      }
+      first = false;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = (g + u * step) * R::kRows + sub;
+      float xa[N], xb[N];
+      Vec16<T>::unpack(ra[u], xa);
+      Vec16<T>::unpack(rb[u], xb);
+      const float r = eps > 0.f ? row_rstd<D, N, R::kLanes>(xa, xb, eps) : 1.f;
+      if (h >= heads || !store) continue;
+      float ya[N], yb[N];
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        float p0, p1, q0, q1;
+        fastmath::fmul2(p0, p1, xa[e], xa[e + 1], r, r);
+        fastmath::fmul2(q0, q1, xb[e], xb[e + 1], r, r);
+        fastmath::fmul2(ya[e], ya[e + 1], p0, p1, ac[e], ac[e + 1]);
+        fastmath::ffma2(ya[e], ya[e + 1], q0, q1, bs[e], bs[e + 1], ya[e], ya[e + 1]);
+        fastmath::fmul2(yb[e], yb[e + 1], q0, q1, bc[e], bc[e + 1]);
+        fastmath::ffma2(yb[e], yb[e + 1], p0, p1, as[e], as[e + 1], yb[e], yb[e + 1]);
+      }
+      T* out = dst + (int64_t)h * pitch;
+      store_n<T>(out + c * N, ya);
+      store_n<T>(out + D / 2 + c * N, yb);
+    }
+  }
+}
+
+// Warps a token's row groups are dealt to: one, unless the tokens alone leave the SMs without
+// enough warps; never more than there are groups.
+inline int head_split(int64_t n_tok, int groups) {
+  const int64_t want = (int64_t)sm_count() * 32;
+  int s = 1;
+  while (s < groups && n_tok * s < want) s *= 2;
+  return s < groups ? s : groups;
+}
+// First group at or after `from` that part `part` of `split` takes.
+__device__ __forceinline__ int first_group(int from, int part, int split) {
+  return from + (part - from % split + split) % split;
 }
 
 }  // namespace msa
