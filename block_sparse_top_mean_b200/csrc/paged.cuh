@@ -74,11 +74,11 @@ int paged_grid();                     // CTAs of a schedule: one an SM
 // record of the devices where that happened).
 cudaError_t raise_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>* done);
 // Each kernel takes the sequences with a.min_new .. a.max_new new tokens, whatever their rows.
-// rows: the row tile asked for (at least G).  few: bf16; f32: fp32.
-cudaError_t launch_paged_few(const HeadShape& s, PagedAttn a, int rows, const void* q,
+// rows: the row tile asked for (at least G).  step: bf16, up to 16 rows; f32: fp32; chunk: bf16
+// on the tensor cores, row tiles of 2 x 128 rows.
+cudaError_t launch_paged_step(const HeadShape& s, PagedAttn a, int rows, const void* q,
                              const void* kp, const void* vp, void* o, float* lse,
                              const struct PagedParts& parts, int* err, cudaStream_t st);
-// chunk: bf16 on the tensor cores, row tiles of 2 x 128 rows.
 cudaError_t launch_paged_chunk(const HeadShape& s, PagedAttn a, const void* q, const void* kp,
                                const void* vp, void* o, float* lse,
                                const struct PagedParts& parts, int* err, cudaStream_t st);

@@ -13,8 +13,7 @@
 //                   product that reads P_X from the same columns;
 //   two warpgroups  the softmax of one half each, one thread a row: scores from TMEM, base-2
 //                   exponentials, P back to TMEM as bf16 (rounded once, 2^-9 of each weight).  The exponent reference moves only
-//                   when a row's maximum outgrows it by 2^8, so O is rarely rescaled.  (The
-//                   maximum is that of the raw scores: the scale must not be negative.)
+//                   when a row's maximum outgrows it by 2^8, so O is rarely rescaled.
 // TMEM columns: S_0 / P_0 [0, 128), S_1 / P_1 [128, 256), O_0 [256, ..), O_1 [384, ..).
 // Keys behind the last visible one: their scores are replaced, and the issuer clears their V
 // rows (which may hold anything) before the product.
@@ -75,7 +74,7 @@ __device__ __forceinline__ int halves(const PagedAttn& a, const Run& r) {
 
 // One row's softmax over a tile: scores (TMEM columns s_t ..) to weights (bf16, over them), the
 // row's reference and sum brought along.  lim: the tile's keys that the row sees; FULL: all, in
-// every row of the warp.  started: O (o_t ..) holds earlier tiles.  p_part[0] is arrived at when
+// every row of the warp, and c2 >= 0 (the maximum of unscaled scores serves).  started: O (o_t ..) holds earlier tiles.  p_part[0] is arrived at when
 // the first half of the weights is in place, p_part[1] when all are.
 template <bool FULL, int D>
 __device__ __forceinline__ void softmax_tile(uint32_t s_t, uint32_t o_t, float c2, int lim,
@@ -110,6 +109,14 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_t, uint32_t o_t, float c
         for (int k = 0; k < 32; ++k)
           if (hf * 64 + w * 32 + k < lim) mx = fmaxf(mx, __uint_as_float(sv[hf * 2 + w][k]));
     }
+  }
+  if (!FULL && c2 < 0.f) {                                // the scaled maximum is at the minimum
+    mx = CUDART_INF_F;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (w * 32 + k < lim) mx = fminf(mx, __uint_as_float(sv[w][k]));
   }
   const float mc = FULL || lim > 0 ? mx * c2 : -CUDART_INF_F;
   const bool need = mc > mref + kRescaleLog2;
@@ -394,7 +401,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
           if (!wait(sm, &sm.s_full[x], steps & 1, err)) { ok = false; break; }
           tc_fence_after();
           // (two bodies: with the mask's comparisons in one, every column paid for them)
-          if (__all_sync(0xffffffffu, lim == KT))
+          if (__all_sync(0xffffffffu, lim == KT && c2 >= 0.f))
             softmax_tile<true, D>(s_t, o_t, c2, lim, i > 0, mref, l, sm.p_full[x]);
           else
             softmax_tile<false, D>(s_t, o_t, c2, lim, i > 0, mref, l, sm.p_full[x]);

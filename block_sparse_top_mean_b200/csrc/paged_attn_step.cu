@@ -1,22 +1,17 @@
-// Attention of a few new tokens over a paged cache, bf16 (see paged.cuh for the schedule).
+// Attention of single new tokens (up to 16 rows) over a paged cache, bf16 (see paged.cuh for the
+// schedule and paged_ring.cuh for the stream).
 //
-// With R = new tokens x G rows against a cache, 4 R flops come with every element of K and V:
-// up to R of about 64 the cache's stream from HBM is the bound, and the kernels are built round
-// it.  A producer warp walks the CTA's run of (row tile, 32-key tile) pairs and copies each
-// tile's K and V rows by tensor maps over the pools (128-byte swizzle, one box for every run of
-// keys that a page holds) into a ring of stages; page numbers are fetched 32 pieces ahead.
-// Four consumer warps run both products on mma.sync m16n8k16 (the tensor pipe is far from its
-// limit at these row counts, and a tcgen05 tile would be 128 rows):
-//   paged_step_kernel (R <= 16): a tile belongs to one warp, so four tiles are in work at a
-//     time and a tile takes one pass of the softmax.  The products are S^T = K Q^T and
-//     O^T += V^T P^T: keys and dims fill the 16 rows of the instruction and the queries its 8
-//     columns, so up to 8 rows waste nothing (queries as the 16 rows took twice the
-//     instructions).  The warps' outputs are joined in shared memory when the item ends.
-//     Weights go into the product with V as two bf16 terms (hi + lo, 2^-17): the second
-//     product hides behind HBM, and the output is off by its own rounding alone.
-//   paged_few_kernel (R <= 64): a warp owns 16 of 64 rows and reads every tile; weights are
-//     rounded to bf16 once (2^-9 of each, as elsewhere in this library; 64 rows x two terms
-//     would no longer hide).
+// With R = new tokens x G rows against a cache, 4 R flops come with every element of K and V: the
+// cache's stream from HBM is the bound, and the kernel is built round it.  Four consumer warps
+// run both products on mma.sync m16n8k16 (the tensor pipe is far from its limit, and a tcgen05
+// tile would be 128 rows).  A tile belongs to one warp, so four tiles are in work at a time and a
+// tile takes one pass of the softmax.  The products are S^T = K Q^T and O^T += V^T P^T: keys and
+// dims fill the 16 rows of the instruction and the queries its 8 columns, so up to 8 rows waste
+// nothing (queries as the 16 rows took twice the instructions).  The warps' outputs are joined
+// in shared memory when the item ends.  Weights go into the product with V as two bf16 terms
+// (hi + lo, 2^-17): the second product hides behind HBM, and the output is off by its own
+// rounding alone.
+//   64 sequences x 8192 keys, 32 / 8 heads of 128: 325 us, 6.6 TB/s; 1 x 131072 keys: 87 us.
 // Keys behind the last visible one are not loaded past their page piece; their scores are
 // replaced, and their V rows (which may hold anything) masked in the fragments.
 #include "paged_ring.cuh"
@@ -62,10 +57,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Byte offset of 16-byte chunk c (8 dims each) of key row r inside a K or V tile.
-__device__ __forceinline__ uint32_t tile_off(int r, int c) {
-  return (uint32_t)(c >> 3) * kSlice + (uint32_t)r * 128u + ((uint32_t)((c & 7) ^ (r & 7)) << 4);
-}
 // Clears the bf16 lanes of a fragment word whose keys (k, k + 1) are not below lim.
 __device__ __forceinline__ uint32_t keep_keys(uint32_t w, int k, int lim) {
   return k + 1 < lim ? w : k < lim ? w & 0xffffu : 0u;
@@ -74,7 +65,7 @@ __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
 }
 
-// ------------------------------------------------------------------ up to 8 * NQ rows
+// Up to 8 * NQ rows.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -315,228 +306,38 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
   } while (run_next<KT>(a, r));
 }
 
-// ------------------------------------------------------------------ up to 64 rows
-template <int D, int ST>
-__global__ void __launch_bounds__(kThreads, 1)
-paged_few_kernel(const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, int box,
-                 const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ o,
-                 float* __restrict__ lse, PagedParts parts, int* err,
-                 const __grid_constant__ PagedAttn a) {
-  constexpr int R = 64;
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* ring = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Ring<ST, kConsumers>& sm = *reinterpret_cast<Ring<ST, kConsumers>*>(ring + ST * kStageBytes<D, 2>);
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  Run r = begin<kThreads>(tm_k, tm_v, sm, kConsumers, parts, a);
-  if (r.at >= r.end) return;
-  if (warp == kConsumers) {
-    produce<D, 2>(tm_k, tm_v, box, ring, sm, r, err, a);
-    return;
-  }
-  const int gr = lane >> 2, t4 = lane & 3, mi = lane >> 3, ri = lane & 7;
-  const int row0 = warp * 16 + gr;           // this thread's rows: row0, row0 + 8
-  int st = 0;
-  uint32_t phase = 0;
-  bool first_item = true, aborted = false;
-  do {
-    const int tile0 = run_first(a, r), nt = run_tiles(a, r), vis = tile_keys(a, r.v, r.rt);
-    if (nt == 0) break;                                   // the run ends in the item's lead
-    int see[2];
-    bool there[2];                                        // rows that hold a query
-    uint32_t qa[D / 16][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = row0 + 8 * i, t_in = r.rt * a.tt + row / a.G;
-      const bool on = row < a.tt * a.G && t_in < r.v.n;
-      there[i] = on;
-      see[i] = on ? (int)max(0LL, min((long long)r.v.past + t_in + 1, (long long)r.v.cap)) : 0;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(
-          q + (r.v.tok0 + t_in) * a.qs + (int64_t)(r.g * a.G + row % a.G) * D);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        qa[ks][i] = on ? __ldg(src + ks * 8 + t4) : 0u;
-        qa[ks][2 + i] = on ? __ldg(src + ks * 8 + 4 + t4) : 0u;
-      }
-    }
-    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
-    float acc[D / 8][4];
-#pragma unroll
-    for (int dt = 0; dt < D / 8; ++dt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[dt][e] = 0.f;
-
-    for (int it = 0; it < nt; ++it) {
-      if (aborted || !ring_wait(sm, &sm.full[st], phase, err)) {
-        aborted = true;
-        break;
-      }
-      const uint32_t sk = smem_u32(ring + st * kStageBytes<D, 2>), sv = sk + kTileBytes<D, 2>;
-      const int key0 = (tile0 + it) * KT;
-      float s[KT / 8][4];
-#pragma unroll
-      for (int nt8 = 0; nt8 < KT / 8; ++nt8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt8][e] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ks += 2)
-#pragma unroll
-        for (int nt8 = 0; nt8 < KT / 8; ++nt8) {
-          uint32_t b[4];
-          ldsm4(sk + tile_off(nt8 * 8 + ri, 2 * ks + mi), b);
-          mma16816(s[nt8], qa[ks], b[0], b[1]);
-          mma16816(s[nt8], qa[ks + 1], b[2], b[3]);
-        }
-      // online softmax of rows row0 and row0 + 8 over the tile's 32 keys
-      // (rows that hold no query need no mask: their results go nowhere)
-      const bool inside = __all_sync(0xffffffffu, (!there[0] || key0 + KT <= see[0]) &&
-                                                      (!there[1] || key0 + KT <= see[1]));
-      float ref[2], alpha[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float mx = -CUDART_INF_F;
-#pragma unroll
-        for (int nt8 = 0; nt8 < KT / 8; ++nt8)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = s[nt8][2 * i + e] * a.scale_log2;
-            if (!inside && key0 + nt8 * 8 + 2 * t4 + e >= see[i]) x = -CUDART_INF_F;
-            s[nt8][2 * i + e] = x;
-            mx = fmaxf(mx, x);
-          }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[i], mx);
-        ref[i] = mn == -CUDART_INF_F ? 0.f : mn;
-        alpha[i] = fast_exp2(m[i] - ref[i]);
-        m[i] = mn;
-        float add = 0.f;
-#pragma unroll
-        for (int nt8 = 0; nt8 < KT / 8; ++nt8)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float p = fast_exp2(s[nt8][2 * i + e] - ref[i]);
-            s[nt8][2 * i + e] = p;
-            add += p;
-          }
-        l[i] = l[i] * alpha[i] + add;
-      }
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-        for (int dt = 0; dt < D / 8; ++dt) {
-          acc[dt][0] *= alpha[0];
-          acc[dt][1] *= alpha[0];
-          acc[dt][2] *= alpha[1];
-          acc[dt][3] *= alpha[1];
-        }
-      }
-      const int lim = vis - key0;                         // keys of the tile that exist
-#pragma unroll
-      for (int kk = 0; kk < KT / 16; ++kk) {
-        uint32_t ph[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {                     // (row, key half): (0,0) (1,0) (0,1) (1,1)
-          const float p0 = s[2 * kk + (w >> 1)][2 * (w & 1)];
-          const float p1 = s[2 * kk + (w >> 1)][2 * (w & 1) + 1];
-          ph[w] = pack_bf16x2(p0, p1);
-        }
-#pragma unroll
-        for (int dt = 0; dt < D / 8; dt += 2) {
-          uint32_t b[4];
-          ldsm4_t(sv + tile_off(kk * 16 + (mi & 1) * 8 + ri, dt + (mi >> 1)), b);
-          if (lim < KT) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) b[w] = keep_keys(b[w], kk * 16 + (w & 1) * 8 + 2 * t4, lim);
-          }
-          mma16816(acc[dt], ph, b[0], b[1]);
-          mma16816(acc[dt + 1], ph, b[2], b[3]);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.empty[st]);
-      if (++st == ST) {
-        st = 0;
-        phase ^= 1;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    }
-    const bool whole = nt == r.tiles;
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (first_item ? 0 : 1);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = row0 + 8 * i, t_in = r.rt * a.tt + row / a.G;
-      if (row >= a.tt * a.G || t_in >= r.v.n) continue;
-      const int64_t qrow = (r.v.tok0 + t_in) * a.hq + r.g * a.G + row % a.G;
-      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
-#pragma unroll
-      for (int dt = 0; dt < D / 8; ++dt) {
-        const float x = acc[dt][2 * i], y = acc[dt][2 * i + 1];
-        const int c = dt * 8 + 2 * t4;
-        if (whole)
-          *reinterpret_cast<uint32_t*>(o + qrow * D + c) = pack_bf16x2(x * inv, y * inv);
-        else
-          *reinterpret_cast<float2*>(parts.o + (slot * R + row) * D + c) = make_float2(x, y);
-      }
-      if (t4 == 0) {
-        if (!whole) parts.ml[slot * R + row] = make_float2(m[i], l[i]);
-        else if (lse != nullptr)
-          lse[qrow] = l[i] > 0.f ? (m[i] + log2f(l[i])) * kLn2 : -CUDART_INF_F;
-      }
-    }
-    if (!whole && tile0 == 0 && tid == 0)
-      parts.rec[blockIdx.x] = item_record(a, r, first_item);
-    first_item = false;
-  } while (run_next<KT>(a, r));
-}
-
-template <typename K>
-cudaError_t run(K kernel, std::atomic<uint64_t>* done, int rows, size_t smem, PagedAttn& a, const HeadShape& s, const void* q,
-                const void* kp, const void* vp, void* o, float* lse, const PagedParts& parts,
-                int* err, cudaStream_t st) {
-  a.tt = rows / a.G;
+template <int D, int NQ, int ST>
+cudaError_t run(PagedAttn& a, const HeadShape& s, const void* q, const void* kp, const void* vp,
+                void* o, float* lse, const PagedParts& parts, int* err, cudaStream_t st) {
+  a.tt = 8 * NQ / a.G;
   a.lead = kLead;
   int box = 0;
   CUtensorMap mk{}, mv{};
   if (!pool_maps(a, s, kp, vp, &mk, &mv, &box)) return cudaErrorInvalidValue;
-  cudaError_t e = raise_smem((const void*)kernel, smem, done);
+  constexpr size_t smem = ring_bytes<D, 2, ST, kConsumers>() + sizeof(Join<D, 8 * NQ>);
+  static_assert(smem <= 232448, "227 KB a CTA");
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = raise_smem((const void*)paged_step_kernel<D, NQ, ST>, smem, &done);
   if (e != cudaSuccess) return e;
   const int grid = paged_grid();
-  kernel<<<grid, kThreads, smem, st>>>(mk, mv, box, (const __nv_bfloat16*)q, (__nv_bfloat16*)o,
-                                       lse, parts, err, a);
+  paged_step_kernel<D, NQ, ST><<<grid, kThreads, smem, st>>>(
+      mk, mv, box, (const __nv_bfloat16*)q, (__nv_bfloat16*)o, lse, parts, err, a);
   e = cudaGetLastError();
-  return e == cudaSuccess ? launch_paged_combine(s, a, grid, rows, parts, o, lse, st) : e;
-}
-
-template <int D>
-cudaError_t run_rows(int rows, PagedAttn& a, const HeadShape& s, const void* q, const void* kp,
-                     const void* vp, void* o, float* lse, const PagedParts& parts, int* err,
-                     cudaStream_t st) {
-  constexpr int ST = 12 * 128 / D;                    // 192 KB of tiles
-  static std::atomic<uint64_t> done[3];
-  if (rows <= 8)
-    return run(paged_step_kernel<D, 1, ST>, &done[0], 8, ring_bytes<D, 2, ST, kConsumers>() + sizeof(Join<D, 8>), a, s, q,
-               kp, vp, o, lse, parts, err, st);
-  if (rows <= 16) {
-    constexpr int ST2 = D == 128 ? 8 : ST;                // room for 16 rows of four warps
-    return run(paged_step_kernel<D, 2, ST2>, &done[1], 16, ring_bytes<D, 2, ST2, kConsumers>() + sizeof(Join<D, 16>), a, s,
-               q, kp, vp, o, lse, parts, err, st);
-  }
-  return run(paged_few_kernel<D, ST>, &done[2], 64, ring_bytes<D, 2, ST, kConsumers>(), a, s, q, kp, vp, o, lse, parts, err,
-             st);
+  return e == cudaSuccess ? launch_paged_combine(s, a, grid, 8 * NQ, parts, o, lse, st) : e;
 }
 
 }  // namespace
 
-cudaError_t launch_paged_few(const HeadShape& s, PagedAttn a, int rows, const void* q,
-                             const void* kp, const void* vp, void* o, float* lse,
-                             const PagedParts& parts, int* err, cudaStream_t st) {
-  return s.d == 128 ? run_rows<128>(rows, a, s, q, kp, vp, o, lse, parts, err, st)
-                    : run_rows<64>(rows, a, s, q, kp, vp, o, lse, parts, err, st);
+// Stages: 192 KB of tiles (8 of 16 KB measured 1% slower); 128 KB where 16 rows of four 128-wide
+// outputs have to be joined.
+cudaError_t launch_paged_step(const HeadShape& s, PagedAttn a, int rows, const void* q,
+                              const void* kp, const void* vp, void* o, float* lse,
+                              const PagedParts& parts, int* err, cudaStream_t st) {
+  if (s.d == 128)
+    return rows <= 8 ? run<128, 1, 12>(a, s, q, kp, vp, o, lse, parts, err, st)
+                     : run<128, 2, 8>(a, s, q, kp, vp, o, lse, parts, err, st);
+  return rows <= 8 ? run<64, 1, 24>(a, s, q, kp, vp, o, lse, parts, err, st)
+                   : run<64, 2, 24>(a, s, q, kp, vp, o, lse, parts, err, st);
 }
 
 }  // namespace msa

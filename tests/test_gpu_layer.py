@@ -246,6 +246,7 @@ SEQS = {
     "empties": [(0, 0), (2, 2), (0, 77), (5, 3), (1, 1), (0, 0)],      # 5 new, 3 in the cache
     "prompt": [(300, 300)],
     "long_chunk": [(257, 1500)],
+    "mixed": [(1, 300), (1, 17), (150, 800), (1, 1), (0, 40), (2, 90), (3, 3)],
     "verify": [(4, 260), (4, 9), (4, 64)],
 }
 HEADS = {   # dtype, d, hq, hkv, page
