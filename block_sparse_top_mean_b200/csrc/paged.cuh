@@ -119,7 +119,7 @@ __device__ __forceinline__ SeqView load_seq(const PagedAttn& a, int s) {
   SeqView v;
   const int64_t c0 = max((int64_t)0, min((int64_t)__ldg(a.g.cu + s), a.n_tok));
   const int64_t c1 = max(c0, min((int64_t)__ldg(a.g.cu + s + 1), a.n_tok));
-  const int len = __ldg(a.g.kv_lens + s);
+  const int len = max(0, __ldg(a.g.kv_lens + s));
   const int64_t room = a.g.max_pages * a.g.page;
   v.tok0 = c0;
   v.n = (int)(c1 - c0);
@@ -128,15 +128,16 @@ __device__ __forceinline__ SeqView load_seq(const PagedAttn& a, int s) {
   v.n_rt = v.n < a.min_new || v.n > a.max_new ? 0 : (v.n + a.tt - 1) / a.tt;
   return v;
 }
-// Keys that the last token of row tile rt sees.
+// Keys that the last token of row tile rt sees.  (32 bits hold it: past + n is the length.)
 __device__ __forceinline__ int tile_keys(const PagedAttn& a, const SeqView& v, int rt) {
-  const int64_t last = (int64_t)v.past + min((int64_t)v.n, (int64_t)(rt + 1) * a.tt);
-  return (int)max((int64_t)0, min(last, (int64_t)v.cap));
+  const int toks = (int)min((uint32_t)v.n, (uint32_t)(rt + 1) * (uint32_t)a.tt);
+  return max(0, min(v.past + toks, v.cap));
 }
 template <int KT>
 __device__ __forceinline__ int key_tiles(const PagedAttn& a, const SeqView& v, int rt) {
-  return max(1, (tile_keys(a, v, rt) + KT - 1) / KT);
+  return max(1, (int)(((uint32_t)tile_keys(a, v, rt) + KT - 1) / KT));
 }
+
 // sum_{i < n} floor((p i + q) / m) for 0 <= p, q and p (n - 1) + q < 2^31 (the Euclidean
 // algorithm on lattice points under a line: Graham, Knuth, Patashnik, Concrete Mathematics, 3.5).
 __device__ __forceinline__ int64_t floor_sum(int n, uint32_t m, uint32_t p, uint32_t q) {
@@ -164,21 +165,21 @@ __device__ __forceinline__ int64_t floor_sum(int n, uint32_t m, uint32_t p, uint
 // reach cap as many as cap fills, the ones between as ceil of an arithmetic progression.
 template <int KT>
 __device__ __forceinline__ int64_t rows_cost(const PagedAttn& a, const SeqView& v, int k) {
-  if (k <= 4) {                       // (a generated token, a short chunk)
-    int64_t t = (int64_t)k * a.lead;
-    for (int rt = 0; rt < k; ++rt) t += key_tiles<KT>(a, v, rt);
-    return t;
-  }
-  const int64_t past = v.past;
-  // row tiles that end at or before KT, and before cap
-  const int64_t one = min((int64_t)k, max((int64_t)0, (KT - past) / a.tt));
-  const int64_t to = min((int64_t)k, max(one, (max((int64_t)0, v.cap - past) + a.tt - 1) / a.tt - 1));
-  const int full = max(1, (v.cap + KT - 1) / KT);
   int64_t t = (int64_t)k * a.lead;
+  if (k <= 16) {                      // (cheaper than the closed form's divisions)
+    int sum = 0;                      // below 2^31: 16 rows of at most 2^31 / KT tiles
+    for (int rt = 0; rt < k; ++rt) sum += key_tiles<KT>(a, v, rt);
+    return t + sum;
+  }
   if (v.cap <= KT) return t + k;      // every row tile counts one
-  t += one + (k - to) * full;
+  // row tiles that end at or before KT, and before cap
+  const uint32_t tt = a.tt;
+  const int one = min(k, v.past >= KT ? 0 : (int)((uint32_t)(KT - v.past) / tt));
+  const int before = v.cap <= v.past ? 0 : (int)(((uint32_t)(v.cap - v.past) + tt - 1) / tt) - 1;
+  const int to = min(k, max(one, before));
+  t += one + (int64_t)(k - to) * ((v.cap + KT - 1) / KT);
   if (to > one)
-    t += floor_sum((int)(to - one), KT, a.tt, (uint32_t)(past + (one + 1) * a.tt + KT - 1));
+    t += floor_sum(to - one, KT, tt, (uint32_t)v.past + (uint32_t)(one + 1) * tt + KT - 1);
   return t;
 }
 template <int KT>

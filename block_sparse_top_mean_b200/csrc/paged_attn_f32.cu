@@ -7,9 +7,9 @@
 //     at a time, so scores take three shuffles and K and V are read once from shared memory
 //     for four rows of registers.
 //   paged_rows32_kernel (64 rows): 2 d flops a row and key against 74 TFLOP/s make the fp32 pipe
-//     the bound.  A thread holds two rows: 2 x 4 scores from six 16-byte reads for 32
-//     multiply-adds, and D / 4 of its rows' outputs.  A row belongs to eight lanes of one
-//     warp, so the warps meet only at the ring.
+//     the bound, if shared memory can feed it: a thread holds four rows, so eight 16-byte reads
+//     serve 64 multiply-adds (with two rows the reads were 79% busy and the fp32 pipe 32%).  A
+//     row belongs to eight lanes of one warp, so the warps meet only at the ring.
 #include "paged_ring.cuh"
 
 namespace msa {
@@ -254,13 +254,14 @@ paged_step32_kernel(const __grid_constant__ CUtensorMap tm_k,
 }
 
 // ------------------------------------------------------------------ 64 rows
-constexpr int kRowWarps = 8;
+constexpr int kXR = 4;                // rows of a thread
+constexpr int kRowWarps = 64 / kXR / 4;
 constexpr int kRowThreads = 32 * (kRowWarps + 1);
 template <int D> constexpr int kRowStages = 2 * 128 / D;       // 64 KB: two CTAs an SM
 
 template <int D>
 struct __align__(16) Rows32 {
-  float q[64][D + 4];                 // +4: the four row pairs of a warp hit different banks
+  float q[64][D + 4];                 // +4: the rows of a warp's four threads hit different banks
   float p[64][KT + 4];
 };
 
@@ -270,7 +271,7 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, int box,
                     const float* __restrict__ q, float* __restrict__ o, float* __restrict__ lse,
                     PagedParts parts, int* err, const __grid_constant__ PagedAttn a) {
-  constexpr int R = 64, ST = kRowStages<D>, NS = D / 32;
+  constexpr int R = 64, ST = kRowStages<D>, NS = D / 32, X = kXR;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* ring = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -284,34 +285,38 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
     produce<D, 4>(tm_k, tm_v, box, ring, sm, r, err, a);
     return;
   }
-  const int row0 = tid / 8 * 2, tx = tid % 8;   // rows row0, row0 + 1; keys tx + 8 j
+  // rows row0 + 4 x (a warp's four threads in neighbouring rows); keys tx + 8 j
+  const int row0 = warp * 4 * X + lane / 8, tx = lane % 8;
   int st = 0;
   uint32_t phase = 0;
   bool first_item = true, aborted = false;
   do {
     const int tile0 = run_first(a, r), nt = run_tiles(a, r), vis = tile_keys(a, r.v, r.rt);
     if (nt == 0) break;                                   // the run ends in the item's lead
-    int see[2];
+    int see[X];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {                         // (rows of this warp alone)
-      see[x] = row_sees(a, r, row0 + x);
+    for (int x = 0; x < X; ++x) {                         // (rows of this warp alone)
+      const int row = row0 + 4 * x;
+      see[x] = row_sees(a, r, row);
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int c = (i * 8 + tx) * 4;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (see[x] >= 0)
-          y = __ldg(reinterpret_cast<const float4*>(row_query(a, r, q, row0 + x, D) + c));
-        *reinterpret_cast<float4*>(&rs.q[row0 + x][c]) = make_float4(
+        if (see[x] >= 0) y = __ldg(reinterpret_cast<const float4*>(row_query(a, r, q, row, D) + c));
+        *reinterpret_cast<float4*>(&rs.q[row][c]) = make_float4(
             y.x * a.scale_log2, y.y * a.scale_log2, y.z * a.scale_log2, y.w * a.scale_log2);
       }
     }
     __syncwarp();
-    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
-    float4 acc[2][NS];
+    float m[X], l[X];
+    float4 acc[X][NS];
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < X; ++x) {
+      m[x] = -CUDART_INF_F;
+      l[x] = 0.f;
 #pragma unroll
       for (int i = 0; i < NS; ++i) acc[x][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     for (int it = 0; it < nt; ++it) {
       if (aborted || !ring_wait(sm, &sm.full[st], phase, err)) {
         aborted = true;
@@ -320,26 +325,28 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
       const unsigned char* sk = ring + st * kStageBytes<D, 4>;
       const unsigned char* sv = sk + kTileBytes<D, 4>;
       const int key0 = (tile0 + it) * KT, lim = vis - key0;
-      float s[2][4];
+      float s[X][4];
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < X; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[x][j] = 0.f;
 #pragma unroll 1
       for (int i = 0; i < NS; ++i)
 #pragma unroll 2
         for (int c = 0; c < 8; ++c) {
-          const float4 q0 = *reinterpret_cast<const float4*>(&rs.q[row0][i * 32 + c * 4]);
-          const float4 q1 = *reinterpret_cast<const float4*>(&rs.q[row0 + 1][i * 32 + c * 4]);
+          float4 y[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 y = lds4(sk + i * kSlice + (j * 8 + tx) * 128 + ((c ^ tx) << 4));
-            s[0][j] = dot4(q0, y, s[0][j]);
-            s[1][j] = dot4(q1, y, s[1][j]);
+          for (int j = 0; j < 4; ++j)
+            y[j] = lds4(sk + i * kSlice + (j * 8 + tx) * 128 + ((c ^ tx) << 4));
+#pragma unroll
+          for (int x = 0; x < X; ++x) {
+            const float4 qx = *reinterpret_cast<const float4*>(&rs.q[row0 + 4 * x][i * 32 + c * 4]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[x][j] = dot4(qx, y[j], s[x][j]);
           }
         }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < X; ++x) {
         float mx = m[x];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -355,7 +362,7 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float e = exp2f(s[x][j] - ref);
-          rs.p[row0 + x][j * 8 + tx] = e;
+          rs.p[row0 + 4 * x][j * 8 + tx] = e;
           add += e;
         }
         l[x] = l[x] * alpha + add;
@@ -366,23 +373,35 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
       }
       __syncwarp();
-      // (weights of keys behind the last are zero, but their V rows may hold anything)
-      const int keys = min(KT, lim);
-#pragma unroll 1
-      for (int k = 0; k < keys; k += 4) {
-        const float4 p0 = *reinterpret_cast<const float4*>(&rs.p[row0][k]);
-        const float4 p1 = *reinterpret_cast<const float4*>(&rs.p[row0 + 1][k]);
-        const float w0[4] = {p0.x, p0.y, p0.z, p0.w}, w1[4] = {p1.x, p1.y, p1.z, p1.w};
+      // four keys: their weights for the thread's rows, and the V rows
+      auto keys4 = [&](int k, int n) {
+        float w[X][4];
+#pragma unroll
+        for (int x = 0; x < X; ++x) {
+          const float4 p = *reinterpret_cast<const float4*>(&rs.p[row0 + 4 * x][k]);
+          w[x][0] = p.x;
+          w[x][1] = p.y;
+          w[x][2] = p.z;
+          w[x][3] = p.w;
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (k + e >= keys) break;
+          if (e >= n) break;
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
             const float4 y = lds4(sv + i * kSlice + (k + e) * 128 + ((tx ^ ((k + e) & 7)) << 4));
-            fma4(acc[0][i], w0[e], y);
-            fma4(acc[1][i], w1[e], y);
+#pragma unroll
+            for (int x = 0; x < X; ++x) fma4(acc[x][i], w[x][e], y);
           }
         }
+      };
+      if (lim >= KT) {
+#pragma unroll 1
+        for (int k = 0; k < KT; k += 4) keys4(k, 4);
+      } else {
+        // (weights of keys behind the last are zero, but their V rows may hold anything)
+#pragma unroll 1
+        for (int k = 0; k < lim; k += 4) keys4(k, lim - k);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[st]);
@@ -394,13 +413,14 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
     const bool whole = nt == r.tiles;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (first_item ? 0 : 1);
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < X; ++x) {
 #pragma unroll
       for (int w = 1; w < 8; w <<= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], w);
       if (see[x] < 0) continue;
-      const int64_t qrow = row_out(a, r, row0 + x);
+      const int row = row0 + 4 * x;
+      const int64_t qrow = row_out(a, r, row);
       const float inv = whole ? (l[x] > 0.f ? 1.f / l[x] : 0.f) : 1.f;
-      float* dst = whole ? o + qrow * D : parts.o + (slot * R + row0 + x) * D;
+      float* dst = whole ? o + qrow * D : parts.o + (slot * R + row) * D;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const float4 y = acc[x][i];
@@ -408,7 +428,7 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
             make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
       }
       if (tx == 0) {
-        if (!whole) parts.ml[slot * R + row0 + x] = make_float2(m[x], l[x]);
+        if (!whole) parts.ml[slot * R + row] = make_float2(m[x], l[x]);
         else if (lse != nullptr)
           lse[qrow] = l[x] > 0.f ? (m[x] + log2f(l[x])) * kLn2 : -CUDART_INF_F;
       }
