@@ -7,72 +7,127 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Joins the parts of the item that CTA blockIdx.x began and did not finish.  WARPS warps a
-// row, each over every WARPS-th part, joined in order; the parts come from L2, so what counts
-// is the chain record -> maxima -> outputs, and that it starts while the attention kernel
-// still runs (programmatic dependent launch: the wait below is for that kernel's results).
-template <typename T, int D, int WARPS>
+// Join the parts of the item that CTA blockIdx.x began and did not finish, in their order:
+// with m the largest of the parts' maxima, o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+// The parts come from L2, so what counts is the chain record -> maxima -> outputs, and that it
+// starts as the attention kernel ends (programmatic dependent launch: the wait is for that
+// kernel's results).
+__device__ __forceinline__ int64_t part_slot(const int4& rec, int i) {
+  return i == 0 ? 2 * (int64_t)blockIdx.x + (rec.z & 1) : 2 * ((int64_t)blockIdx.x + i);
+}
+
+__device__ __forceinline__ int64_t part_qrow(const int4& rec, int row, int G, int hq) {
+  return ((int64_t)rec.y << 32 | (uint32_t)rec.x) + (int64_t)(row / G) * hq + row % G;
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void store_joined(T* o, float* lse, int64_t qrow, int lane,
+                                             const float (&acc)[D / 32], float mx, float l) {
+  constexpr int E = D / 32;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[qrow * D + lane * E + e] = from_f32<T>(acc[e] * inv);
+  if (lane == 0 && lse != nullptr)
+    lse[qrow] = l != 0.f ? (mx + log2f(l)) * kLn2 : -CUDART_INF_F;
+}
+
+template <int E>
+__device__ __forceinline__ void load_part(float (&y)[E], const float* src) {
+  if (E == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(src);
+  else *reinterpret_cast<float2*>(y) = *reinterpret_cast<const float2*>(src);
+}
+
+// Few rows: an item may have a part from every CTA.  A block a row, each of its eight warps
+// over every eighth part.
+template <typename T, int D>
 __global__ void __launch_bounds__(256)
-paged_combine_kernel(PagedParts parts, int rows, T* __restrict__ o, float* __restrict__ lse,
-                     int G, int hq) {
-  constexpr int E = D / 32;           // columns of a lane
-  constexpr int RB = 8 / WARPS;       // rows of a block
-  __shared__ float s_acc[8][D];
-  __shared__ float s_l[8];
+paged_combine_parts_kernel(PagedParts parts, int rows, T* __restrict__ o,
+                           float* __restrict__ lse, int G, int hq) {
+  constexpr int E = D / 32, W = 8;    // columns of a lane, warps
+  __shared__ float s_acc[W][D];
+  __shared__ float s_l[W];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 rec = parts.rec[blockIdx.x];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wr = warp % WARPS;
-  const int row = blockIdx.y * RB + warp / WARPS;
-  if (rec.w == 0 || (int)(blockIdx.y * RB) >= (rec.z >> 1) * G) return;   // whole block
-  const bool on = row < (rec.z >> 1) * G;
-  const int n = on ? rec.w : 0;
-  const int64_t slot0 = 2 * (int64_t)blockIdx.x + (rec.z & 1);
-  auto slot = [&](int i) -> int64_t { return i == 0 ? slot0 : 2 * ((int64_t)blockIdx.x + i); };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y, n = rec.w;
+  if (n == 0 || row >= (rec.z >> 1) * G) return;          // whole block
+  float2 ml = make_float2(-CUDART_INF_F, 0.f);
+  float y[E] = {};
+  if (warp < n) {                                         // before the maximum is known
+    const int64_t at = part_slot(rec, warp) * rows + row;
+    ml = parts.ml[at];
+    load_part<E>(y, parts.o + at * D + lane * E);
+  }
   float mx = -CUDART_INF_F;
-  for (int i = lane; i < n; i += 32) mx = fmaxf(mx, parts.ml[slot(i) * rows + row].x);
+  for (int i = lane; i < n; i += 32)
+    mx = fmaxf(mx, parts.ml[part_slot(rec, i) * rows + row].x);
   mx = warp_max(mx);
   const float ref = mx == -CUDART_INF_F ? 0.f : mx;
-  float l = 0.f, acc[E];
+  float w = exp2f(ml.x - ref), l = ml.y * w, acc[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int e = 0; e < E; ++e) acc[e] = y[e] * w;
 #pragma unroll 4
-  for (int i = wr; i < n; i += WARPS) {
-    const float2 ml = parts.ml[slot(i) * rows + row];
-    const float* src = parts.o + (slot(i) * rows + row) * D + lane * E;
-    float y[E];
-    if (E == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(src);
-    else *reinterpret_cast<float2*>(y) = *reinterpret_cast<const float2*>(src);
+  for (int i = warp + W; i < n; i += W) {
+    const int64_t at = part_slot(rec, i) * rows + row;
+    ml = parts.ml[at];
+    load_part<E>(y, parts.o + at * D + lane * E);
+    w = exp2f(ml.x - ref);
+    l = fmaf(ml.y, w, l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(y[e], w, acc[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < W; ++w) {
+    l += s_l[w];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += s_acc[w][lane * E + e];
+  }
+  store_joined<T, D>(o, lse, part_qrow(rec, row, G, hq), lane, acc, mx, l);
+}
+
+// Many rows, few parts each: a warp a row, which asks for its first two parts (a cut item has
+// two) before it knows their maxima.  (Two and four rows a warp: no faster.)
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+paged_combine_rows_kernel(PagedParts parts, int rows, T* __restrict__ o,
+                          float* __restrict__ lse, int G, int hq) {
+  constexpr int E = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 rec = parts.rec[blockIdx.x];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = rec.w;
+  const int row = blockIdx.y * 8 + warp;
+  if (n == 0 || row >= (rec.z >> 1) * G) return;
+  const int64_t at0 = part_slot(rec, 0) * rows + row, at1 = part_slot(rec, 1) * rows + row;
+  const float2 m0 = parts.ml[at0], m1 = parts.ml[at1];
+  float acc[E], y[E];
+  load_part<E>(acc, parts.o + at0 * D + lane * E);
+  load_part<E>(y, parts.o + at1 * D + lane * E);
+  float mx = fmaxf(m0.x, m1.x);
+  for (int i = 2; i < n; ++i) mx = fmaxf(mx, parts.ml[part_slot(rec, i) * rows + row].x);
+  const float ref = mx == -CUDART_INF_F ? 0.f : mx;
+  const float w0 = exp2f(m0.x - ref), w1 = exp2f(m1.x - ref);
+  float l = fmaf(m1.y, w1, m0.y * w0);
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = fmaf(y[e], w1, acc[e] * w0);
+  for (int i = 2; i < n; ++i) {
+    const int64_t at = part_slot(rec, i) * rows + row;
+    const float2 ml = parts.ml[at];
+    load_part<E>(y, parts.o + at * D + lane * E);
     const float w = exp2f(ml.x - ref);
     l = fmaf(ml.y, w, l);
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = fmaf(y[e], w, acc[e]);
   }
-  if (WARPS > 1) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-    if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    if (wr != 0) return;
-#pragma unroll
-    for (int w = 1; w < WARPS; ++w) {
-      l += s_l[warp + w];
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += s_acc[warp + w][lane * E + e];
-    }
-  }
-  if (!on) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int64_t qrow = ((int64_t)rec.y << 32 | (uint32_t)rec.x) + (int64_t)(row / G) * hq + row % G;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[qrow * D + lane * E + e] = from_f32<T>(acc[e] * inv);
-  if (lane == 0 && lse != nullptr)
-    lse[qrow] = l > 0.f ? (mx + log2f(l)) * kLn2 : -CUDART_INF_F;
+  store_joined<T, D>(o, lse, part_qrow(rec, row, G, hq), lane, acc, mx, l);
 }
 
 template <typename T, int D>
 cudaError_t run_combine(const PagedAttn& a, int grid, int rows, const PagedParts& parts, void* o,
                         float* lse, cudaStream_t st) {
-  // few rows may have a part from every CTA: eight warps a row; large row tiles have few parts
   const bool few = rows <= 16;
   const int used = a.tt * a.G;
   cudaLaunchConfig_t cfg{};
@@ -84,9 +139,9 @@ cudaError_t run_combine(const PagedAttn& a, int grid, int rows, const PagedParts
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, D, 8>, parts, rows, (T*)o, lse,
-                                  a.G, a.hq)
-             : cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, D, 1>, parts, rows, (T*)o, lse,
+  return few ? cudaLaunchKernelEx(&cfg, paged_combine_parts_kernel<T, D>, parts, rows, (T*)o,
+                                  lse, a.G, a.hq)
+             : cudaLaunchKernelEx(&cfg, paged_combine_rows_kernel<T, D>, parts, rows, (T*)o, lse,
                                   a.G, a.hq);
 }
 

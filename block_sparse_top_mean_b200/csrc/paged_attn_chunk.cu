@@ -412,7 +412,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
         const int64_t qrow = (r.v.tok0 + t_in) * a.hq + r.g * a.G + h;
         const int prow = x * half_toks * a.G + row;       // = token of the tile * G + head
         const int64_t slot = 2 * (int64_t)blockIdx.x + (first_item ? 0 : 1);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t ov[32];
@@ -448,7 +448,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
         if (on) {
           if (!whole) parts.ml[slot * kPagedMaxRows + prow] = make_float2(mref, l);
           else if (lse != nullptr)
-            lse[qrow] = l > 0.f ? (mref + log2f(l)) * kLn2 : -CUDART_INF_F;
+            lse[qrow] = l != 0.f ? (mref + log2f(l)) * kLn2 : -CUDART_INF_F;
         }
       }
       if (!whole && tile0 == 0 && tid == 0) parts.rec[blockIdx.x] = item_record(a, r, first_item);

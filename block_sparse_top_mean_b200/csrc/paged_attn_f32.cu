@@ -236,11 +236,11 @@ paged_step32_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
       const int64_t qrow = row_out(a, r, row);
       if (whole) {
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
         *reinterpret_cast<float4*>(o + qrow * D + c) =
             make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
         if (c == 0 && lse != nullptr)
-          lse[qrow] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -CUDART_INF_F;
+          lse[qrow] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -CUDART_INF_F;
       } else {
         *reinterpret_cast<float4*>(parts.o + (slot * R + row) * D + c) = y;
         if (c == 0) parts.ml[slot * R + row] = make_float2(mx, sum);
@@ -419,7 +419,7 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (see[x] < 0) continue;
       const int row = row0 + 4 * x;
       const int64_t qrow = row_out(a, r, row);
-      const float inv = whole ? (l[x] > 0.f ? 1.f / l[x] : 0.f) : 1.f;
+      const float inv = whole ? (l[x] != 0.f ? 1.f / l[x] : 0.f) : 1.f;
       float* dst = whole ? o + qrow * D : parts.o + (slot * R + row) * D;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
@@ -430,7 +430,7 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (tx == 0) {
         if (!whole) parts.ml[slot * R + row] = make_float2(m[x], l[x]);
         else if (lse != nullptr)
-          lse[qrow] = l[x] > 0.f ? (m[x] + log2f(l[x])) * kLn2 : -CUDART_INF_F;
+          lse[qrow] = l[x] != 0.f ? (m[x] + log2f(l[x])) * kLn2 : -CUDART_INF_F;
       }
     }
     if (!whole && tile0 == 0 && tid == 0)

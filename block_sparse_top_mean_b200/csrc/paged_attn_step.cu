@@ -289,11 +289,11 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
       const int64_t qrow = (r.v.tok0 + t_in) * a.hq + r.g * a.G + row % a.G;
       if (whole) {
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
         *reinterpret_cast<uint2*>(o + qrow * D + c) =
             make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
         if (c == 0 && lse != nullptr)
-          lse[qrow] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -CUDART_INF_F;
+          lse[qrow] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -CUDART_INF_F;
       } else {
         *reinterpret_cast<float4*>(parts.o + (slot * R + row) * D + c) = y;
         if (c == 0) parts.ml[slot * R + row] = make_float2(mx, sum);

@@ -337,6 +337,20 @@ def test_paged_attn_large_scores_and_infinite_lse(msa):
     st.check(*st.attn(msa, max_new=1))
 
 
+@pytest.mark.parametrize("dtype,new,kv", [
+    (torch.bfloat16, 2, 300), (torch.bfloat16, 1, 9000), (torch.bfloat16, 90, 700),
+    (torch.float32, 2, 300), (torch.float32, 90, 700)])
+def test_paged_attn_nan_query_stays_in_its_row(msa, dtype, new, kv):
+    """A query head that is NaN has a NaN output and lse; every other row is as without it."""
+    st = Step(dtype, 128, 4, 1, 64, [(new, kv)])
+    o, lse = st.attn(msa)
+    st.q[new // 2, 1] = float("nan")
+    o2, lse2 = st.attn(msa)
+    assert o2[new // 2, 1].isnan().all() and lse2[new // 2, 1].isnan()
+    o2[new // 2, 1], lse2[new // 2, 1] = o[new // 2, 1], lse[new // 2, 1]
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 APPEND = [   # heads, seqs, base, norm, weighted, queries
     ("bf16_g4", "chunks", 1e6, True, True, True),
     ("bf16_g8_p16", "steps", 1e4, False, False, True),
