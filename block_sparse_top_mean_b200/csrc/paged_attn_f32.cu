@@ -6,18 +6,24 @@
 //     belongs to one of three warps; eight lanes share a key (16 dims each at d = 128), four keys
 //     at a time, so scores take three shuffles and K and V are read once from shared memory
 //     for four rows of registers.
-//   paged_rows32_kernel (64 rows): 2 d flops a row and key against 74 TFLOP/s make the fp32 pipe
+//     16 sequences x 8192 keys, 32 / 8 heads of 128: 189 us, 5.7 TB/s.
+//   paged_rows32_kernel (64 rows): 4 d flops a row and key against 74 TFLOP/s make the fp32 pipe
 //     the bound, if shared memory can feed it: a thread holds four rows, so eight 16-byte reads
-//     serve 64 multiply-adds (with two rows the reads were 79% busy and the fp32 pipe 32%).  A
-//     row belongs to eight lanes of one warp, so the warps meet only at the ring.
+//     serve 64 multiply-adds (with two rows the reads were 79% busy and the fp32 pipe 32%), two
+//     in an instruction (1330 -> 1130 us).  A row belongs to eight lanes of one warp, so the
+//     warps meet only at the ring.  A prompt of 2048 tokens, 32 / 8 heads of 128: 1009 us, 34
+//     TFLOP/s; the accumulators leave room for two warps a scheduler.
 #include "paged_ring.cuh"
+#include "fastmath.cuh"
 
 namespace msa {
 namespace {
 
 using namespace paged;
+using fastmath::ffma2;
 
-constexpr int kLead = 4;              // cost of an item beside its tiles, in tiles
+// Cost of an item beside its tiles, in tiles.
+constexpr int kStepLead = 4, kRowLead = 1;
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float4 lds4(const unsigned char* p) {
@@ -28,6 +34,10 @@ __device__ __forceinline__ void fma4(float4& d, float s, const float4& v) {
   d.y = fmaf(s, v.y, d.y);
   d.z = fmaf(s, v.z, d.z);
   d.w = fmaf(s, v.w, d.w);
+}
+__device__ __forceinline__ void fma4_pairs(float4& d, float s, const float4& v) {
+  ffma2(d.x, d.y, s, s, v.x, v.y, d.x, d.y);
+  ffma2(d.z, d.w, s, s, v.z, v.w, d.z, d.w);
 }
 __device__ __forceinline__ float dot4(const float4& a, const float4& b, float s) {
   return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s))));
@@ -325,14 +335,14 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
       const unsigned char* sk = ring + st * kStageBytes<D, 4>;
       const unsigned char* sv = sk + kTileBytes<D, 4>;
       const int key0 = (tile0 + it) * KT, lim = vis - key0;
-      float s[X][4];
+      float s[X][4], s2[X][4];                            // over even and over odd dims
 #pragma unroll
       for (int x = 0; x < X; ++x)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[x][j] = 0.f;
+        for (int j = 0; j < 4; ++j) s[x][j] = s2[x][j] = 0.f;
 #pragma unroll 1
       for (int i = 0; i < NS; ++i)
-#pragma unroll 2
+#pragma unroll 8
         for (int c = 0; c < 8; ++c) {
           float4 y[4];
 #pragma unroll
@@ -342,7 +352,10 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
           for (int x = 0; x < X; ++x) {
             const float4 qx = *reinterpret_cast<const float4*>(&rs.q[row0 + 4 * x][i * 32 + c * 4]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[x][j] = dot4(qx, y[j], s[x][j]);
+            for (int j = 0; j < 4; ++j) {
+              ffma2(s[x][j], s2[x][j], qx.x, qx.y, y[j].x, y[j].y, s[x][j], s2[x][j]);
+              ffma2(s[x][j], s2[x][j], qx.z, qx.w, y[j].z, y[j].w, s[x][j], s2[x][j]);
+            }
           }
         }
 #pragma unroll
@@ -350,6 +363,7 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
         float mx = m[x];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          s[x][j] += s2[x][j];
           if (key0 + j * 8 + tx >= see[x]) s[x][j] = -CUDART_INF_F;
           mx = fmaxf(mx, s[x][j]);
         }
@@ -391,12 +405,12 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
           for (int i = 0; i < NS; ++i) {
             const float4 y = lds4(sv + i * kSlice + (k + e) * 128 + ((tx ^ ((k + e) & 7)) << 4));
 #pragma unroll
-            for (int x = 0; x < X; ++x) fma4(acc[x][i], w[x][e], y);
+            for (int x = 0; x < X; ++x) fma4_pairs(acc[x][i], w[x][e], y);
           }
         }
       };
       if (lim >= KT) {
-#pragma unroll 1
+#pragma unroll 2
         for (int k = 0; k < KT; k += 4) keys4(k, 4);
       } else {
         // (weights of keys behind the last are zero, but their V rows may hold anything)
@@ -445,7 +459,7 @@ cudaError_t run(K kernel, std::atomic<uint64_t>* done, int rows, int threads, in
                 const void* vp, void* o, float* lse, const PagedParts& parts, int* err,
                 cudaStream_t st) {
   a.tt = rows / a.G;
-  a.lead = kLead;
+  a.lead = rows == 64 ? kRowLead : kStepLead;
   int box = 0;
   CUtensorMap mk{}, mv{};
   if (!pool_maps(a, s, kp, vp, &mk, &mv, &box)) return cudaErrorInvalidValue;
