@@ -64,6 +64,8 @@ def _rows(name, x, T, d, dtype, index):
     if stride[2] != 1 or stride[1] != d:
         if x.numel() and (stride[2] != 1 or shape[1] > 1):
             _fail(f"{name}: the heads of a token must be packed (only the token stride is free)")
+    if T > 1 and stride[0] == 0:                          # (0 stands for packed tokens below)
+        _fail(f"{name}: tokens must not share their storage")
     return stride[0] if T > 1 else shape[1] * d
 
 

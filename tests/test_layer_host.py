@@ -171,3 +171,18 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
                  lambda: msa.paged_workspace(q, pool, lens)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_binding_refuses_tokens_that_share_storage():
+    """A token stride of 0 stands for packed tokens in the C entries: an expanded tensor, whose
+    stride is 0, would be read past its end.  The check needs no GPU (device index -1)."""
+    from block_sparse_top_mean_b200.layer import _rows
+    one = torch.zeros(1, 2, 64)
+    assert _rows("q", one, 1, 64, torch.float32, -1) == 128
+    assert _rows("q", torch.zeros(4, 6, 64)[:, 2:4], 4, 64, torch.float32, -1) == 384
+    with pytest.raises(ValueError, match="share"):
+        _rows("q", one.expand(4, 2, 64), 4, 64, torch.float32, -1)
+    with pytest.raises(ValueError, match="packed"):
+        _rows("q", torch.zeros(4, 1, 64).expand(4, 2, 64), 4, 64, torch.float32, -1)
+    with pytest.raises(ValueError, match="packed"):
+        _rows("q", torch.zeros(4, 64, 2).transpose(1, 2), 4, 64, torch.float32, -1)
