@@ -15,8 +15,9 @@
 namespace msa {
 namespace {
 
-constexpr int kWarps = 2;             // 8 CTAs an SM: 57 us for 11.5K tokens, 60 with 8 warps a CTA
+constexpr int kCtas = 16;             // warps of an SM, a CTA each (8 CTAs of 2 warps: 3% slower)
 constexpr int kUnroll = 4;            // row groups of the queries in flight per warp
+constexpr int kValues = 2;            // and of the values
 
 struct AppendArgs {
   Turns tn;
@@ -27,17 +28,20 @@ struct AppendArgs {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32, 8)
+__global__ void __launch_bounds__(32, kCtas)
 paged_append_kernel(const T* q, const T* k, const T* v, const T* __restrict__ wq,
                     const T* __restrict__ wk, T* __restrict__ kp, T* __restrict__ vp, T* qo,
                     int* err, const __grid_constant__ AppendArgs a) {
   using R = RowLayout<T, D>;
   constexpr int N = R::N;
-  const int lane = threadIdx.x & 31, c = lane % R::kLanes, sub = lane / R::kLanes;
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t t = unit / a.split;
-  if (t >= a.n_tok) return;                               // whole warp
-  const int part = (int)(unit - t * a.split);
+  const int lane = threadIdx.x, c = lane % R::kLanes, sub = lane / R::kLanes;
+  const int64_t t = blockIdx.x / a.split;
+  const int part = (int)(blockIdx.x - t * a.split);
+  if (a.split == 1 && lane < 3) {
+    const T* row = lane == 0 ? q + t * a.qs : lane == 1 ? k + t * a.ks : v + t * a.vs;
+    const int heads = lane == 0 ? a.hq : a.hkv;
+    if (heads > 0) prefetch_rows(row, heads * (int64_t)(D * sizeof(T)));
+  }
   const int gq = (a.hq + R::kRows - 1) / R::kRows, gk = (a.hkv + R::kRows - 1) / R::kRows;
   int64_t slot = -1, pos = 0;                             // row of KV head 0 in the pools
   bool placed = false, angles = false, mine = false;
@@ -74,8 +78,23 @@ paged_append_kernel(const T* q, const T* k, const T* v, const T* __restrict__ wq
                               place(cs, sn);
                               return mine;
                             });
-  // (where the keys go is known only after find(): the rows are placed from the slot)
+  // The values are copied: their rows are asked for before the keys' turn, kValues groups at a
+  // time, and stored behind it.
   const int g0 = first_group(gq, part, a.split) - gq;
+  int gv = first_group(gq + gk, part, a.split) - gq - gk;
+  uint4 va[kValues], vb[kValues];
+  auto load_values = [&]() {
+#pragma unroll
+    for (int u = 0; u < kValues; ++u) {
+      const int h = (gv + u * a.split) * R::kRows + sub;
+      if (h >= a.hkv) continue;
+      const T* row = v + t * a.vs + (int64_t)h * D;
+      va[u] = ld16_once(row + c * N);
+      vb[u] = ld16_once(row + D / 2 + c * N);
+    }
+  };
+  load_values();
+  // (where the keys go is known only after find(): the rows are placed from the slot)
   if (g0 < gk) {
     find();
     turn_heads<T, D, 2>(k + t * a.ks, kp + max(slot, (int64_t)0) * D, a.g.page * D, a.hkv, wk,
@@ -84,20 +103,18 @@ paged_append_kernel(const T* q, const T* k, const T* v, const T* __restrict__ wq
                           return slot >= 0;
                         });
   }
-  // values are copied
-  for (int g = first_group(gq + gk, part, a.split) - gq - gk; g < gk; g += a.split) {
-    const int h = g * R::kRows + sub;
-    const T* row = v + t * a.vs + (int64_t)h * D;
-    uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
-    if (h < a.hkv) {
-      ra = ld16_once(row + c * N);
-      rb = ld16_once(row + D / 2 + c * N);
-    }
+  while (gv < gk) {
     find();                                               // (all lanes)
-    if (slot < 0 || h >= a.hkv) continue;
-    T* out = vp + (slot + (int64_t)h * a.g.page) * D;
-    *reinterpret_cast<uint4*>(out + c * N) = ra;
-    *reinterpret_cast<uint4*>(out + D / 2 + c * N) = rb;
+#pragma unroll
+    for (int u = 0; u < kValues; ++u) {
+      const int h = (gv + u * a.split) * R::kRows + sub;
+      if (slot < 0 || h >= a.hkv) continue;
+      T* out = vp + (slot + (int64_t)h * a.g.page) * D;
+      *reinterpret_cast<uint4*>(out + c * N) = va[u];
+      *reinterpret_cast<uint4*>(out + D / 2 + c * N) = vb[u];
+    }
+    gv += kValues * a.split;
+    load_values();
   }
 }
 
@@ -106,8 +123,7 @@ cudaError_t run(AppendArgs& a, const void* q, const void* k, const void* v, cons
                 const void* wk, void* kp, void* vp, void* qo, int* err, cudaStream_t st) {
   constexpr int kR = RowLayout<T, D>::kRows;
   a.split = head_split(a.n_tok, (a.hq + kR - 1) / kR + 2 * ((a.hkv + kR - 1) / kR));
-  const int64_t grid = (a.n_tok * a.split + kWarps - 1) / kWarps;
-  paged_append_kernel<T, D><<<(unsigned)grid, kWarps * 32, 0, st>>>(
+  paged_append_kernel<T, D><<<(unsigned)(a.n_tok * a.split), 32, 0, st>>>(
       (const T*)q, (const T*)k, (const T*)v, (const T*)wq, (const T*)wk, (T*)kp, (T*)vp, (T*)qo,
       err, a);
   return cudaGetLastError();

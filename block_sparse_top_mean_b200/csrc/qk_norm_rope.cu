@@ -62,6 +62,10 @@ qk_norm_rope_kernel(const T* q, const T* k, const int32_t* __restrict__ cu,
   const int64_t t = unit / a.split;
   if (t >= a.n_tok) return;                               // whole warp
   const int part = (int)(unit - t * a.split);
+  if (a.split == 1 && (threadIdx.x & 31) == 0) {
+    prefetch_rows(q + t * a.qs, a.hq * (int64_t)(D * sizeof(T)));
+    prefetch_rows(k + t * a.ks, a.hkv * (int64_t)(D * sizeof(T)));
+  }
   const int gq = (a.hq + R::kRows - 1) / R::kRows, gk = (a.hkv + R::kRows - 1) / R::kRows;
   float cs0[N], sn0[N];
   bool placed = false;
@@ -120,6 +124,10 @@ qk_norm_rope_bwd_kernel(const TG* __restrict__ dq, const TG* __restrict__ dk,
   for (int64_t unit = (int64_t)cta * kWarps + warp; unit < units;
        unit += (int64_t)n_cta * kWarps) {
     const int64_t t = unit / split;
+    if (split == 1 && lane == 0) {
+      prefetch_rows(x0 + t * stride, heads * (int64_t)(D * sizeof(T)));
+      prefetch_rows(y0 + t * heads * D, heads * (int64_t)(D * sizeof(TG)));
+    }
     const T* xt = x0 + t * stride + c * N;
     const TG* gt = y0 + t * heads * D + c * N;
     T* ot = o0 + t * heads * D + c * N;
