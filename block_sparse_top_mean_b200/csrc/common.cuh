@@ -26,6 +26,12 @@ __device__ __forceinline__ uint4 ldg16_stream(const void* p) {
   return r;
 }
 
+// Asks for `bytes` (a multiple of 16) at p, 16-byte aligned, to be brought to L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, int64_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"((uint32_t)bytes)
+               : "memory");
+}
+
 __device__ __forceinline__ float bf16lo_to_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi_to_f32(uint32_t w) {
   return __uint_as_float(w & 0xffff0000u);

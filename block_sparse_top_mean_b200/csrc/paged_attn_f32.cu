@@ -87,7 +87,7 @@ paged_step32_kernel(const __grid_constant__ CUtensorMap tm_k,
   Run r = begin<kStepThreads>(tm_k, tm_v, sm, 1, parts, a);
   if (r.at >= r.end) return;
   if (warp == kStepWarps) {
-    produce<D, 4>(tm_k, tm_v, box, ring, sm, r, err, a);
+    produce<D, 4>(tm_k, tm_v, box, ring, sm, r, err, q, a);
     return;
   }
   const int kg = lane >> 3, l8 = lane & 7;      // key of each four; dims l8 * 4 of each 32
@@ -292,7 +292,7 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
   Run r = begin<kRowThreads>(tm_k, tm_v, sm, kRowWarps, parts, a);
   if (r.at >= r.end) return;
   if (warp == kRowWarps) {
-    produce<D, 4>(tm_k, tm_v, box, ring, sm, r, err, a);
+    produce<D, 4>(tm_k, tm_v, box, ring, sm, r, err, q, a);
     return;
   }
   // rows row0 + 4 x (a warp's four threads in neighbouring rows); keys tx + 8 j

@@ -89,7 +89,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
   Run r = begin<kThreads>(tm_k, tm_v, sm, 1, parts, a);
   if (r.at >= r.end) return;
   if (warp == kConsumers) {
-    produce<D, 2>(tm_k, tm_v, box, ring, sm, r, err, a);
+    produce<D, 2>(tm_k, tm_v, box, ring, sm, r, err, q, a);
     return;
   }
   // thread (gr, t4) of a warp: scores of keys gr, gr + 8 of a 16-key block and queries 2 t4,

@@ -52,11 +52,12 @@ __device__ __forceinline__ bool ring_wait(Ring<ST, W>& sm, uint64_t* bar, uint32
   return false;
 }
 
-// The producer warp: copies every tile of the run, in order.
+// The producer warp: copies every tile of the run, in order.  It is ahead of the consumers, so it
+// also asks for an item's queries to L2 (256 short sequences: 52 -> 50 us).
 template <int D, int E, int ST, int W>
 __device__ __forceinline__ void produce(const CUtensorMap& tm_k, const CUtensorMap& tm_v, int box,
                                         unsigned char* ring, Ring<ST, W>& sm, Run r, int* err,
-                                        const PagedAttn& a) {
+                                        const void* q, const PagedAttn& a) {
   const int lane = threadIdx.x % 32;
   const int per = KT / box;                               // page pieces of a tile
   const int rows = (int)(a.g.n_pages * a.hkv * a.g.page);
@@ -66,6 +67,9 @@ __device__ __forceinline__ void produce(const CUtensorMap& tm_k, const CUtensorM
   do {
     const int tile0 = run_first(a, r), nt = run_tiles(a, r), vis = tile_keys(a, r.v, r.rt);
     if (nt == 0) break;                                   // the run ends in the item's lead
+    for (int t = r.rt * a.tt + lane; t < min(r.v.n, (r.rt + 1) * a.tt); t += 32)
+      prefetch_l2((const char*)q + ((r.v.tok0 + t) * a.qs + (int64_t)r.g * a.G * D) * E,
+                  a.G * D * E);
     // row of piece i of the item's part of this run in the pools, `rows` (reads as zeros)
     // for an entry that is no page, -1 past the last visible key
     auto piece_row = [&](int i) -> int {

@@ -126,14 +126,6 @@ __device__ __forceinline__ uint4 ld16_once(const void* p) {
                : "l"(p));
   return r;
 }
-// Asks for `bytes` (a multiple of 16) at p to be brought to L2.  A warp works through a token's
-// heads with as many rows in flight as its registers hold; one instruction at its start has
-// the rest of them on the way (32K tokens: forward 116 -> 106 us, gradient 235 -> 216, append
-// of 11.5K tokens 55 -> 52).  The rows of the warp's next token asked for as well: slower.
-__device__ __forceinline__ void prefetch_rows(const void* p, int64_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"((uint32_t)bytes)
-               : "memory");
-}
 // Loads N elements of T at p into fp32 (the 8 fp32 gradients of a bf16 chunk take two loads).
 template <typename T, int N>
 __device__ __forceinline__ void load_n(const T* p, float* f) {
