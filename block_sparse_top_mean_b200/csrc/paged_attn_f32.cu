@@ -3,10 +3,11 @@
 // library are (a tf32 product would keep 11 bits).
 //
 //   paged_step32_kernel (up to 8 rows, single tokens): the cache's stream is the bound.  A tile
-//     belongs to one of three warps; eight lanes share a key (16 dims each at d = 128), four keys
+//     belongs to one of six warps; eight lanes share a key (16 dims each at d = 128), four keys
 //     at a time, so scores take three shuffles and K and V are read once from shared memory
-//     for four rows of registers.
-//     16 sequences x 8192 keys, 32 / 8 heads of 128: 189 us, 5.7 TB/s.
+//     for four rows of registers.  16 sequences x 8192 keys, 32 / 8 heads of 128: 171 us, 6.3
+//     TB/s (three warps of two stages: 186); with 8 heads a KV head 289 us (467): shuffles and
+//     exponentials of eight rows, which one lane a key instead made no faster (350).
 //   paged_rows32_kernel (64 rows): 4 d flops a row and key against 74 TFLOP/s make the fp32 pipe
 //     the bound, if shared memory can feed it: a thread holds four rows, so eight 16-byte reads
 //     serve 64 multiply-adds (with two rows the reads were 79% busy and the fp32 pipe 32%), two
@@ -58,7 +59,7 @@ __device__ __forceinline__ int64_t row_out(const PagedAttn& a, const Run& r, int
 }
 
 // ------------------------------------------------------------------ up to 4 * RG rows
-constexpr int kStepWarps = 3;          // two stages each
+constexpr int kStepWarps = 6;          // a stage each (d = 64: two)
 constexpr int kStepThreads = 32 * (kStepWarps + 1);
 template <int D> constexpr int kStepStages = 6 * 128 / D;      // 192 KB
 
@@ -191,7 +192,7 @@ paged_step32_kernel(const __grid_constant__ CUtensorMap tm_k,
           for (int i = 0; i < NS; ++i) {
             const float4 v = lds4(sv + i * kSlice + (k >> 1) * 1024 + ((k & 1) ? at1 : at0));
 #pragma unroll
-            for (int x = 0; x < 4; ++x) fma4(acc[g][x][i], s[k][x], v);
+            for (int x = 0; x < 4; ++x) fma4_pairs(acc[g][x][i], s[k][x], v);
           }
         }
       }
