@@ -97,7 +97,7 @@ cudaError_t launch_paged_attn(const HeadShape& s, const PagedShape& g, int64_t m
 size_t layer_ws_bytes(const msa_params* p, int32_t op);
 
 constexpr int kPagedCtas = 160;       // most SMs a schedule uses (a B200 has 148)
-constexpr int kPagedRecs = 2 * kPagedCtas;       // most CTAs: two an SM with row tiles of 64
+constexpr int kPagedRecs = 2 * kPagedCtas;       // most CTAs: two an SM with row tiles of up to 64
 constexpr int kPagedMaxRows = 256;    // rows of the largest row tile (one CTA an SM)
 
 // Workspace body: records, then (maximum, sum) and outputs of the parts.  CTA c's parts: 2c

@@ -11,7 +11,7 @@
 // in shared memory when the item ends.  Weights go into the product with V as two bf16 terms
 // (hi + lo, 2^-17): the second product hides behind HBM, and the output is off by its own
 // rounding alone.
-//   64 sequences x 8192 keys, 32 / 8 heads of 128: 325 us, 6.6 TB/s; 1 x 131072 keys: 87 us.
+//   64 sequences x 8192 keys, 32 / 8 heads of 128: 316 us, 6.8 TB/s; 1 x 131072 keys: 87 us.
 // Keys behind the last visible one are not loaded past their page piece; their scores are
 // replaced, and their V rows (which may hold anything) masked in the fragments.
 #include "paged_ring.cuh"
@@ -25,9 +25,14 @@ using fastmath::fast_exp2;
 
 constexpr int kConsumers = 4;         // warps 0-3; warp 4 produces
 constexpr int kThreads = 32 * (kConsumers + 1);
-// What an item costs beside its tiles, in tiles (48 sequences of 1 to 16384 keys: 0 168 us, 4 71,
-// 7 61, 10 64).
-constexpr int kLead = 7;
+// Two CTAs an SM: while one joins an item's warps and starts the next, the other's tiles keep
+// coming (256 sequences of up to 256 keys 50 -> 35 us, 48 of 1 to 16384 52 -> 49, 64 x 8192 325
+// -> 316; one CTA of 192 KB: the same bytes in flight).
+constexpr int kCtas = 2;
+template <int D> constexpr int kStages = 4 * 128 / D;        // 64 KB of tiles a CTA
+// What an item costs beside its tiles, in tiles (48 sequences of 1 to 16384 keys, one CTA an SM: 0
+// 168 us, 4 71, 7 61, 10 64; two: 3 51, 5 48.5, 6 48.5, 9 49).
+constexpr int kLead = 6;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // The warps' outputs of an item, joined when it ends.
@@ -72,19 +77,21 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-template <int D, int NQ, int ST>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int NQ>
+__global__ void __launch_bounds__(kThreads, kCtas)
 paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, int box,
                   const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ o,
                   float* __restrict__ lse, PagedParts parts, int* err,
                   const __grid_constant__ PagedAttn a) {
-  constexpr int R = 8 * NQ;
+  constexpr int R = 8 * NQ, ST = kStages<D>;
+  using RingT = Ring<ST, kConsumers>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* ring = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Ring<ST, kConsumers>& sm = *reinterpret_cast<Ring<ST, kConsumers>*>(ring + ST * kStageBytes<D, 2>);
-  Join<D, R>& jn = *reinterpret_cast<Join<D, R>*>(ring + ST * kStageBytes<D, 2> + sizeof(Ring<ST, kConsumers>));
+  RingT& sm = *reinterpret_cast<RingT*>(ring + ST * kStageBytes<D, 2>);
+  Join<D, R>& jn =
+      *reinterpret_cast<Join<D, R>*>(ring + ST * kStageBytes<D, 2> + sizeof(RingT));
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   Run r = begin<kThreads>(tm_k, tm_v, sm, 1, parts, a);
   if (r.at >= r.end) return;
@@ -306,7 +313,7 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
   } while (run_next<KT>(a, r));
 }
 
-template <int D, int NQ, int ST>
+template <int D, int NQ>
 cudaError_t run(PagedAttn& a, const HeadShape& s, const void* q, const void* kp, const void* vp,
                 void* o, float* lse, const PagedParts& parts, int* err, cudaStream_t st) {
   a.tt = 8 * NQ / a.G;
@@ -314,13 +321,13 @@ cudaError_t run(PagedAttn& a, const HeadShape& s, const void* q, const void* kp,
   int box = 0;
   CUtensorMap mk{}, mv{};
   if (!pool_maps(a, s, kp, vp, &mk, &mv, &box)) return cudaErrorInvalidValue;
-  constexpr size_t smem = ring_bytes<D, 2, ST, kConsumers>() + sizeof(Join<D, 8 * NQ>);
-  static_assert(smem <= 232448, "227 KB a CTA");
+  constexpr size_t smem = ring_bytes<D, 2, kStages<D>, kConsumers>() + sizeof(Join<D, 8 * NQ>);
+  static_assert(kCtas * (smem + 1024) <= 233472, "228 KB an SM");
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = raise_smem((const void*)paged_step_kernel<D, NQ, ST>, smem, &done);
+  cudaError_t e = raise_smem((const void*)paged_step_kernel<D, NQ>, smem, &done);
   if (e != cudaSuccess) return e;
-  const int grid = paged_grid();
-  paged_step_kernel<D, NQ, ST><<<grid, kThreads, smem, st>>>(
+  const int grid = kCtas * paged_grid();
+  paged_step_kernel<D, NQ><<<grid, kThreads, smem, st>>>(
       mk, mv, box, (const __nv_bfloat16*)q, (__nv_bfloat16*)o, lse, parts, err, a);
   e = cudaGetLastError();
   return e == cudaSuccess ? launch_paged_combine(s, a, grid, 8 * NQ, parts, o, lse, st) : e;
@@ -328,16 +335,14 @@ cudaError_t run(PagedAttn& a, const HeadShape& s, const void* q, const void* kp,
 
 }  // namespace
 
-// Stages: 192 KB of tiles (8 of 16 KB measured 1% slower); 128 KB where 16 rows of four 128-wide
-// outputs have to be joined.
 cudaError_t launch_paged_step(const HeadShape& s, PagedAttn a, int rows, const void* q,
                               const void* kp, const void* vp, void* o, float* lse,
                               const PagedParts& parts, int* err, cudaStream_t st) {
   if (s.d == 128)
-    return rows <= 8 ? run<128, 1, 12>(a, s, q, kp, vp, o, lse, parts, err, st)
-                     : run<128, 2, 8>(a, s, q, kp, vp, o, lse, parts, err, st);
-  return rows <= 8 ? run<64, 1, 24>(a, s, q, kp, vp, o, lse, parts, err, st)
-                   : run<64, 2, 24>(a, s, q, kp, vp, o, lse, parts, err, st);
+    return rows <= 8 ? run<128, 1>(a, s, q, kp, vp, o, lse, parts, err, st)
+                     : run<128, 2>(a, s, q, kp, vp, o, lse, parts, err, st);
+  return rows <= 8 ? run<64, 1>(a, s, q, kp, vp, o, lse, parts, err, st)
+                   : run<64, 2>(a, s, q, kp, vp, o, lse, parts, err, st);
 }
 
 }  // namespace msa
