@@ -205,12 +205,12 @@ cudaError_t launch_paged_attn(const HeadShape& s, const PagedShape& g, int64_t m
     return launch_paged_f32(s, a, rows <= 8 ? (int)rows : 64, q, kp, vp, o, lse, parts, err, st);
   // Up to 16 rows the mma.sync kernel keeps up with the cache's stream; above, the tensor cores'
   // 256-row tiles do better even where few of their rows hold a query (8 sequences x 16000 keys,
-  // 4 heads a group: 4 tokens 93 us on the first, 5 tokens 110 us on the second; mma.sync with 64
-  // rows a tile took 202 us).
+  // 4 heads a group: 2 tokens 87 us on the first, 109 on the second; 4 tokens 96 and 107; 5 tokens
+  // 123 on the second, 202 on mma.sync with 64 rows a tile).
   if (rows <= 16) return launch_paged_step(s, a, (int)rows, q, kp, vp, o, lse, parts, err, st);
   // A chunk among generated tokens (the others' average says so): single tokens would fill a few
   // rows of a 256-row tile each, so they get a launch of their own (48 tokens and a chunk of 1024:
-  // 352 us, 395 us in one launch).
+  // 333 us, 392 us in one launch).
   const int small = a.G <= 8 ? 8 : 16;
   if (g.n_seqs > 1 && a.G <= 16 && (s.n_tok - max_new) * a.G <= 64 * (g.n_seqs - 1)) {
     PagedAttn b = a;

@@ -3,7 +3,7 @@
 //
 // An item's row tile is two halves of 128 rows (128 / G tokens each) against 128-key tiles;
 // 4 d flops a row and key against 2 x 2 d bytes a key keep the tensor cores the bound from a
-// few tens of rows up.  Roles (320 threads, one CTA an SM):
+// few tens of rows up.  Roles (384 threads, two warps of them spare; one CTA an SM):
 //   producer warp   copies K and V tiles by tensor maps over the pools (one box for every run
 //                   of keys that a page holds, page numbers fetched 32 pieces ahead) into a ring
 //                   of 128-key units, and the item's query rows (a box of G heads x tokens);
@@ -12,8 +12,15 @@
 //                   thread run in order, so S_X of the next tile may be issued right behind the
 //                   product that reads P_X from the same columns;
 //   two warpgroups  the softmax of one half each, one thread a row: scores from TMEM, base-2
-//                   exponentials, P back to TMEM as bf16 (rounded once, 2^-9 of each weight).  The exponent reference moves only
+//                   exponentials, P back to TMEM as bf16 (rounded once, 2^-9 of each weight: the
+//                   tensor core takes no wider left operand beside a bf16 V) in two parts, so the
+//                   product with V starts at half of them.  The exponent reference moves only
 //                   when a row's maximum outgrows it by 2^8, so O is rarely rescaled.
+// What bounds it: softmax and products in turn, 2.0 us a tile of 256 x 128 at d = 128 (1.64 with
+// the softmax left out).  2048 tokens over 30720 keys, 32 / 8 heads: 871 us, 1223 TFLOP/s; a
+// prompt of 8192: 459 us; four ragged chunks over 12000 keys in pages of 16: 84 us, of which
+// about 4 us an item's start and end and 8 us the join.  Measured slower: four softmax
+// warpgroups, 64-key tiles with two sets of scores, exponentials on a polynomial.
 // TMEM columns: S_0 / P_0 [0, 128), S_1 / P_1 [128, 256), O_0 [256, ..), O_1 [384, ..).
 // Keys behind the last visible one: their scores are replaced, and the issuer clears their V
 // rows (which may hold anything) before the product.
@@ -34,7 +41,9 @@ constexpr int kIssuer = 8, kProducer = 9;
 constexpr uint32_t kHalf = 128 * 128; // 128 rows x 64 dims
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.f;
-constexpr int kLead = 3;              // cost of an item beside its tiles, in tiles
+// Cost of an item beside its tiles, in tiles (ragged chunks / 2048-token prompt / 8192, a slower
+// join: 2 101 / 74 / 492 us, 3 89 / 68 / 470, 4 86 / 68 / 475, 6 88 / 69 / 484).
+constexpr int kLead = 3;
 
 template <int D> constexpr uint32_t kUnit = KT * D * 2;      // one K or V tile
 template <int D> constexpr int kUnits = D == 128 ? 5 : 10;   // 160 KB
@@ -74,8 +83,9 @@ __device__ __forceinline__ int halves(const PagedAttn& a, const Run& r) {
 
 // One row's softmax over a tile: scores (TMEM columns s_t ..) to weights (bf16, over them), the
 // row's reference and sum brought along.  lim: the tile's keys that the row sees; FULL: all, in
-// every row of the warp, and c2 >= 0 (the maximum of unscaled scores serves).  started: O (o_t ..) holds earlier tiles.  p_part[0] is arrived at when
-// the first half of the weights is in place, p_part[1] when all are.
+// every row of the warp, and c2 >= 0 (the maximum of unscaled scores serves).  started: O (o_t
+// ..) holds earlier tiles.  p_part[0] is arrived at when the first half of the weights is in
+// place, p_part[1] when all are.
 template <bool FULL, int D>
 __device__ __forceinline__ void softmax_tile(uint32_t s_t, uint32_t o_t, float c2, int lim,
                                              bool started, float& mref, float& l,

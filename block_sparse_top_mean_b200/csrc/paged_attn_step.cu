@@ -70,13 +70,13 @@ __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
 }
 
-// Up to 8 * NQ rows.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
+// Up to 8 * NQ rows.
 template <int D, int NQ>
 __global__ void __launch_bounds__(kThreads, kCtas)
 paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -241,7 +241,8 @@ paged_step_kernel(const __grid_constant__ CUtensorMap tm_k,
           ldsm4_t(sv + v_off[dt & 3] + (dt >> 2) * kSlice + kb * 2048, f);
           if (lim < KT) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) f[w] = keep_keys(f[w], kb * 16 + (w >> 1) * 8 + 2 * t4, lim);
+            for (int w = 0; w < 4; ++w)
+              f[w] = keep_keys(f[w], kb * 16 + (w >> 1) * 8 + 2 * t4, lim);
           }
 #pragma unroll
           for (int n = 0; n < NQ; ++n) {

@@ -41,7 +41,8 @@ __device__ __forceinline__ void ring_fail(Ring<ST, W>& sm, int* err) {
 // Waits for a phase of one of the ring's barriers, for the whole warp; false when the wait ran
 // out (after ~2 s) or another warp's did.
 template <int ST, int W>
-__device__ __forceinline__ bool ring_wait(Ring<ST, W>& sm, uint64_t* bar, uint32_t parity, int* err) {
+__device__ __forceinline__ bool ring_wait(Ring<ST, W>& sm, uint64_t* bar, uint32_t parity,
+                                          int* err) {
   bool ok = mbar_try_wait(bar, parity);
   if (__all_sync(0xffffffffu, ok)) return true;
   const long long t0 = clock64();
