@@ -12,7 +12,7 @@
 //                   thread run in order, so S_X of the next tile may be issued right behind the
 //                   product that reads P_X from the same columns;
 //   two warpgroups  the softmax of one half each, one thread a row: scores from TMEM, base-2
-//                   exponentials, P back to TMEM as bf16 (rounded once, 2^-9 of each weight: the
+//                   exponentials, P back to TMEM as bf16 (rounded once, 2^-8 of each weight: the
 //                   tensor core takes no wider left operand beside a bf16 V) in two parts, so the
 //                   product with V starts at half of them.  The exponent reference moves only
 //                   when a row's maximum outgrows it by 2^8, so O is rarely rescaled.
