@@ -14,6 +14,7 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 msa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA; }
 
 constexpr int64_t kMaxTokens = INT32_MAX;
+constexpr int64_t kAhead = 1 << 14;   // 64 pieces of at most 128 keys, and a tile
 constexpr int64_t kMaxGroup = 64;     // query heads of a KV head
 
 msa_status check_heads(const msa_params* p, HeadShape* s) {
@@ -72,8 +73,10 @@ msa_status check_paged(const msa_params* p, const msa_paged_cache* c, HeadShape*
     return MSA_ERR_INVALID_ARG;
   if (p->block % 16 != 0 || p->block > (1 << 20)) return MSA_ERR_UNSUPPORTED;
   if (p->batch >= INT32_MAX || p->seq > kMaxTokens) return MSA_ERR_UNSUPPORTED;
-  // rows of a pool and keys of a table row are counted in 32 bits
-  if (c->n_pages > INT32_MAX / (p->hkv * p->block) || c->max_pages > INT32_MAX / p->block)
+  // rows of a pool and keys of a table row are counted in 32 bits, and the kernels look up to
+  // kAhead keys past the last one
+  if (c->n_pages > INT32_MAX / (p->hkv * p->block) ||
+      c->max_pages > (INT32_MAX - kAhead) / p->block)
     return MSA_ERR_UNSUPPORTED;
   g->table = c->page_table;
   g->kv_lens = c->kv_lens;
@@ -209,7 +212,8 @@ msa_status msa_paged_attn_fwd(const msa_params* p, const msa_paged_cache* cache,
   PagedShape g;
   msa_status st = check_paged(p, cache, &s, &g);
   if (st != MSA_OK) return st;
-  if (!isfinite(p->scale) || max_new < 0) return MSA_ERR_INVALID_ARG;
+  // (the kernels scale to base 2: that factor has to be finite as well)
+  if (!isfinite(p->scale * 1.4426950408889634f) || max_new < 0) return MSA_ERR_INVALID_ARG;
   if (!stride_ok(s, s.hq, &q_stride)) return MSA_ERR_INVALID_ARG;
   if (p->batch == 0 || s.n_tok == 0) return MSA_OK;
   if (q == nullptr || o == nullptr || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4))

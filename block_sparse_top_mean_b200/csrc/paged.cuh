@@ -297,7 +297,7 @@ __device__ __forceinline__ bool run_next(const PagedAttn& a, Run& r) {
     if (++r.g >= a.hkv) {
       r.g = 0;
       do {
-        ++r.s;
+        if (++r.s >= (int)a.g.n_seqs) return false;       // (lengths that changed meanwhile)
         r.v = load_seq(a, r.s);
       } while (r.v.n_rt == 0);
     }

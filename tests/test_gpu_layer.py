@@ -500,6 +500,30 @@ def test_paged_nothing_to_do(msa):
         pad.attn(msa, max_new=0)
 
 
+@pytest.mark.parametrize("dtype,new", [(torch.bfloat16, 1), (torch.bfloat16, 40),
+                                       (torch.float32, 1), (torch.float32, 40)])
+def test_pools_beyond_32_bits(msa, dtype, new):
+    """Pages whose elements lie beyond 2^32 (and bytes beyond 2^33) from the pool's start."""
+    st = Step(dtype, 128, 4, 2, 64, [(new, 200), (new, 64)], spare=0)
+    kp, vp, n = st.kp, st.vp, st.kp.shape[0]
+    total = 2 ** 32 // kp[0].numel() + 2 * n
+    st.kp, st.vp = (torch.empty((total, *kp.shape[1:]), dtype=dtype, device="cuda")
+                    for _ in "kv")
+    st.kp[total - n:], st.vp[total - n:] = kp, vp
+    st.table[st.table >= 0] += total - n
+    st.dev = (_i32(st.table),) + st.dev[1:]
+    ws = msa.paged_workspace(st.q, st.kp, st.dev[1])
+    msa.paged_append(st.k, st.v, st.kp, st.vp, *st.dev, ws=ws)
+    o, lse = st.attn(msa, max_new=new, ws=ws)
+    assert msa.read_device_error(ws) == 0
+    for s, at in ((0, 200), (1, 64)):
+        page, row = st.table[s, (at - 1) // 64], (at - 1) % 64
+        assert torch.equal(st.vp[page, :, row], st.v[st.cu[s + 1] - 1])
+    st.kp, st.vp = st.kp[total - n:].clone(), st.vp[total - n:].clone()
+    st.table[st.table >= 0] -= total - n
+    st.check(o, lse)
+
+
 @pytest.mark.parametrize("new,hq", [(1, 32), (2, 64), (5, 32)])
 def test_paged_attn_long_caches_many_rounds(msa, new, hq):
     """Rings that go round hundreds of times, with copies that arrive late and out of order (a

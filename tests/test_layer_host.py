@@ -106,7 +106,8 @@ def _cache(**kw):
 
 BAD_CACHES = [(dict(k=None), INVALID), (dict(v=4096 + 8), INVALID), (dict(table=None), INVALID),
               (dict(lens=None), INVALID), (dict(cu=4097), INVALID), (dict(n=-1), INVALID), (dict(n=0), INVALID),
-              (dict(m=-1), INVALID), (dict(n=1 << 40), UNSUPPORTED), (dict(m=1 << 40), UNSUPPORTED)]
+              (dict(m=-1), INVALID), (dict(n=1 << 40), UNSUPPORTED), (dict(m=1 << 40), UNSUPPORTED),
+              (dict(m=(2 ** 31 - 1) // 64), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("kw,code", BAD_CACHES)
@@ -152,7 +153,8 @@ def test_paged_refusals(lib):
     assert att(_p(), c, 0, F, 0, F, ctypes.c_void_p(4098), F, need, None) == INVALID
     assert att(_p(), c, -1, F, 0, F, None, F, need, None) == INVALID
     assert att(_p(), c, 0, F, 100, F, None, F, need, None) == INVALID
-    assert att(_p(scale=float("nan")), c, 0, F, 0, F, None, F, need, None) == INVALID
+    for scale in (float("nan"), float("inf"), 3e38):      # 3e38 * log2(e) is no fp32 number
+        assert att(_p(scale=scale), c, 0, F, 0, F, None, F, need, None) == INVALID
     assert att(_p(), c, 0, F, 0, F, None, F, need - 1, None) == WORKSPACE
     assert att(_p(), c, 0, F, 0, F, None, None, need, None) == WORKSPACE
     assert att(_p(seq=0), empty, 0, None, 0, None, None, None, 0, None) == OK
