@@ -188,3 +188,12 @@ def test_binding_refuses_tokens_that_share_storage():
         _rows("q", torch.zeros(4, 1, 64).expand(4, 2, 64), 4, 64, torch.float32, -1)
     with pytest.raises(ValueError, match="packed"):
         _rows("q", torch.zeros(4, 64, 2).transpose(1, 2), 4, 64, torch.float32, -1)
+
+
+def test_packed_images_are_the_structures():
+    """The binding passes msa_params and msa_paged_cache as packed bytes."""
+    from block_sparse_top_mean_b200 import layer
+    a = (3, 1 << 40, 32, 8, 128, 64, 1, 0.125, 1)
+    assert layer._params(*a) == bytes(MsaParams(*a))
+    c = (1 << 47, 2, 3, 4, 5, 1 << 33, 7)
+    assert layer._cache_image(*c) == bytes(MsaPagedCache(*c))
