@@ -51,11 +51,15 @@ paged_append_kernel(const T* q, const T* k, const T* v, const T* __restrict__ wq
   auto find = [&]() {
     if (placed) return;
     placed = true;
-    const int s = warp_segment(a.g.cu, (int)a.g.n_seqs, t);
+    // (the lengths of up to 32 sequences are fetched beside the search)
+    const int n = (int)a.g.n_seqs;
+    const int kv = n <= 32 ? __ldg(a.g.kv_lens + min(lane, n - 1)) : 0;
+    int64_t c0, c1;
+    const int s = warp_segment(a.g.cu, n, t, c0, c1);
     if (s < 0) return;                                    // behind the last sequence
     mine = true;
-    const int64_t c0 = __ldg(a.g.cu + s), c1 = __ldg(a.g.cu + s + 1);
-    pos = (int64_t)__ldg(a.g.kv_lens + s) - (c1 - c0) + (t - c0);
+    const int len = n <= 32 ? __shfl_sync(0xffffffffu, kv, s) : __ldg(a.g.kv_lens + s);
+    pos = (int64_t)len - (c1 - c0) + (t - c0);
     if (pos >= 0 && pos < a.g.max_pages * a.g.page) {
       const int64_t pg = __ldg(a.g.table + (int64_t)s * a.g.max_pages + pos / a.g.page);
       if (pg >= 0 && pg < a.g.n_pages) slot = pg * a.hkv * a.g.page + pos % a.g.page;

@@ -50,8 +50,8 @@ struct NormArgs {
 
 // The token's position in its document (0 for a token no document holds).
 __device__ __forceinline__ int64_t token_pos(const int32_t* cu, int n_docs, int64_t t) {
-  const int s = warp_segment(cu, n_docs, t);
-  return s < 0 ? 0 : t - (int64_t)__ldg(cu + s);
+  int64_t start, end;
+  return warp_segment(cu, n_docs, t, start, end) < 0 ? 0 : t - start;
 }
 
 template <typename T, int D>

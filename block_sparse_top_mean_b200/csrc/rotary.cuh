@@ -34,12 +34,22 @@ struct RowLayout {
 };
 
 // Index of the last segment whose start is <= t: cu[0..n] are the boundaries; -1 for a t
-// outside [cu[0], cu[n]).  One outcome for the warp; 32 probes a round, so up to 1024
-// segments take two dependent loads where a binary search takes ten.  Never reads outside
-// cu[0..n], whatever it holds.
-__device__ __forceinline__ int warp_segment(const int32_t* __restrict__ cu, int n, int64_t t) {
+// outside [cu[0], cu[n]).  One outcome for the warp, start and end its boundaries.  Every lane
+// probes at once: up to 32 segments take one load's latency, up to 1024 three, where a binary
+// search takes ten.  Never reads outside cu[0..n], whatever it holds.
+__device__ __forceinline__ int warp_segment(const int32_t* __restrict__ cu, int n, int64_t t,
+                                            int64_t& start, int64_t& end) {
   const int lane = threadIdx.x & 31;
-  if ((int64_t)__ldg(cu) > t || (int64_t)__ldg(cu + n) <= t) return -1;
+  if (n <= 32) {
+    const int at = min(lane, n - 1);
+    const int c0 = __ldg(cu + at), c1 = __ldg(cu + at + 1);
+    const unsigned in = __ballot_sync(0xffffffffu, lane < n && (int64_t)c0 <= t);
+    const int k = 31 - __clz(in);
+    start = __shfl_sync(0xffffffffu, c0, max(k, 0));
+    end = __shfl_sync(0xffffffffu, c1, max(k, 0));
+    return __shfl_sync(0xffffffffu, c1, n - 1) <= t ? -1 : k;
+  }
+  const int64_t first = __ldg(cu), last = __ldg(cu + n);
   int lo = 0, len = n;
   while (len > 1) {
     const int step = (len + 31) >> 5;
@@ -49,7 +59,9 @@ __device__ __forceinline__ int warp_segment(const int32_t* __restrict__ cu, int 
     lo += k * step;
     len = min(step, len - k * step);
   }
-  return lo;
+  start = __ldg(cu + lo);
+  end = __ldg(cu + lo + 1);
+  return first > t || last <= t ? -1 : lo;
 }
 
 // cos and sin of pair i of a head at position p.
