@@ -37,8 +37,10 @@ Turns make_turns(double base, int d) {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;              // of a CTA of the gradient
 constexpr int kUnroll = 4;            // row groups in flight per warp
+constexpr int kFwdCtas = 16;          // forward: warps of an SM, a CTA each (CTAs of 8: 108 us, not 104)
+constexpr int kFewWarps = 2;          // of a CTA with tokens of few heads
 constexpr int kBwdCtas = 2;           // of the backward kernel on an SM
 
 struct NormArgs {
@@ -55,17 +57,15 @@ __device__ __forceinline__ int64_t token_pos(const int32_t* cu, int n_docs, int6
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+__global__ void __launch_bounds__(32, kFwdCtas)
 qk_norm_rope_kernel(const T* q, const T* k, const int32_t* __restrict__ cu,
                     const T* __restrict__ wq, const T* __restrict__ wk, T* qo, T* ko,
                     const __grid_constant__ NormArgs a) {
   using R = RowLayout<T, D>;
   constexpr int N = R::N;
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t t = unit / a.split;
-  if (t >= a.n_tok) return;                               // whole warp
-  const int part = (int)(unit - t * a.split);
-  if (a.split == 1 && (threadIdx.x & 31) == 0) {
+  const int64_t t = blockIdx.x / a.split;
+  const int part = (int)(blockIdx.x - t * a.split);
+  if (a.split == 1 && threadIdx.x == 0) {
     prefetch_l2(q + t * a.qs, a.hq * (int64_t)(D * sizeof(T)));
     prefetch_l2(k + t * a.ks, a.hkv * (int64_t)(D * sizeof(T)));
   }
@@ -85,6 +85,50 @@ qk_norm_rope_kernel(const T* q, const T* k, const int32_t* __restrict__ cu,
                             place);
   turn_heads<T, D, 2>(k + t * a.ks, ko + t * a.hkv * D, D, a.hkv, wk, a.eps,
                       first_group(gq, part, a.split) - gq, a.split, gk, place);
+}
+
+// Tokens of few heads (up to GQ row groups of queries and GK of keys): all of a token's rows are
+// loaded before its position is looked up, and with fewer registers and CTAs of two warps more
+// tokens are in flight (8 + 1 heads of 64, 32K tokens: 51 -> 22 us; 16 + 4 of 128, 20K: 47 -> 37;
+// two to eight tokens a warp: slower than one).
+template <typename T, int D, int GQ, int GK>
+__global__ void __launch_bounds__(kFewWarps * 32)
+qk_norm_rope_few_kernel(const T* q, const T* k, const int32_t* __restrict__ cu,
+                        const T* __restrict__ wq, const T* __restrict__ wk, T* qo, T* ko,
+                        const __grid_constant__ NormArgs a) {
+  using R = RowLayout<T, D>;
+  constexpr int N = R::N;
+  const int lane = threadIdx.x & 31, c = lane % R::kLanes, sub = lane / R::kLanes;
+  const int64_t t = (int64_t)blockIdx.x * kFewWarps + (threadIdx.x >> 5);
+  if (t >= a.n_tok) return;                               // whole warp
+  uint4 qa[GQ], qb[GQ], ka[GK], kb[GK];
+#pragma unroll
+  for (int g = 0; g < GQ; ++g) {
+    const int h = g * R::kRows + sub;
+    load_row<T, D>(q + t * a.qs + (int64_t)h * D + c * N, h < a.hq, qa[g], qb[g]);
+  }
+#pragma unroll
+  for (int g = 0; g < GK; ++g) {
+    const int h = g * R::kRows + sub;
+    load_row<T, D>(k + t * a.ks + (int64_t)h * D + c * N, h < a.hkv, ka[g], kb[g]);
+  }
+  float cs[N], sn[N], wa[N], wb[N];
+  lane_cos_sin<N, R::kLanes>(a.tn, token_pos(cu, a.n_docs, t), cs, sn);
+  Turn<T, D> turn;
+  load_weights<T, D>(wq, c, wa, wb);
+  turn.set(cs, sn, wa, wb);
+#pragma unroll
+  for (int g = 0; g < GQ; ++g) {
+    const int h = g * R::kRows + sub;
+    turn.row(qa[g], qb[g], a.eps, h < a.hq, qo + (t * a.hq + h) * D + c * N);
+  }
+  load_weights<T, D>(wk, c, wa, wb);
+  turn.set(cs, sn, wa, wb);
+#pragma unroll
+  for (int g = 0; g < GK; ++g) {
+    const int h = g * R::kRows + sub;
+    turn.row(ka[g], kb[g], a.eps, h < a.hkv, ko + (t * a.hkv + h) * D + c * N);
+  }
 }
 
 // ------------------------------------------------------------------ backward
@@ -235,8 +279,22 @@ cudaError_t run_fwd(NormArgs& a, const void* q, const void* k, const int32_t* cu
                     const void* wk, void* qo, void* ko, cudaStream_t st) {
   constexpr int kR = RowLayout<T, D>::kRows;
   a.split = head_split(a.n_tok, (a.hq + kR - 1) / kR + (a.hkv + kR - 1) / kR);
-  const int64_t grid = (a.n_tok * a.split + kWarps - 1) / kWarps;
-  qk_norm_rope_kernel<T, D><<<(unsigned)grid, kWarps * 32, 0, st>>>(
+  const int gq = (a.hq + kR - 1) / kR, gk = (a.hkv + kR - 1) / kR;
+  if (a.split == 1 && gq <= 4 && gk <= 2) {
+    const unsigned few = (unsigned)((a.n_tok + kFewWarps - 1) / kFewWarps);
+    auto launch = [&](auto* kernel) {
+      kernel<<<few, kFewWarps * 32, 0, st>>>((const T*)q, (const T*)k, cu, (const T*)wq,
+                                             (const T*)wk, (T*)qo, (T*)ko, a);
+      return cudaGetLastError();
+    };
+    if (gq == 1) return launch(qk_norm_rope_few_kernel<T, D, 1, 1>);   // (gk <= gq)
+    if (gq == 2)
+      return gk == 1 ? launch(qk_norm_rope_few_kernel<T, D, 2, 1>)
+                     : launch(qk_norm_rope_few_kernel<T, D, 2, 2>);
+    return gk == 1 ? launch(qk_norm_rope_few_kernel<T, D, 4, 1>)
+                   : launch(qk_norm_rope_few_kernel<T, D, 4, 2>);
+  }
+  qk_norm_rope_kernel<T, D><<<(unsigned)(a.n_tok * a.split), 32, 0, st>>>(
       (const T*)q, (const T*)k, cu, (const T*)wq, (const T*)wk, (T*)qo, (T*)ko, a);
   return cudaGetLastError();
 }

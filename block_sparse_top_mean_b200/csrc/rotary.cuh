@@ -155,9 +155,62 @@ __device__ __forceinline__ void store_n(T* p, const float* f) {
   *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(y);
 }
 
+// Norm and rotation of rows at one position.  The weights are folded into the rotation's factors,
+// so an element costs three multiplications: with n = r x, y_a = n_a (w_a cos) - n_b (w_b sin) and
+// y_b = n_b (w_b cos) + n_a (w_a sin).
+template <typename T, int D>
+struct Turn {
+  using R = RowLayout<T, D>;
+  static constexpr int N = R::N;
+  float ac[N], bs[N], bc[N], as[N];   // w_a cos, -w_b sin, w_b cos, w_a sin
+
+  __device__ __forceinline__ void set(const float (&cs)[N], const float (&sn)[N],
+                                      const float (&wa)[N], const float (&wb)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      ac[e] = wa[e] * cs[e];
+      bs[e] = -wb[e] * sn[e];
+      bc[e] = wb[e] * cs[e];
+      as[e] = wa[e] * sn[e];
+    }
+  }
+  // One row, held as (ra, rb) by its lanes, to `out` (this lane's 16 bytes of either half) if
+  // store.  The whole warp calls it.
+  __device__ __forceinline__ void row(const uint4& ra, const uint4& rb, float eps, bool store,
+                                      T* out) const {
+    float xa[N], xb[N];
+    Vec16<T>::unpack(ra, xa);
+    Vec16<T>::unpack(rb, xb);
+    const float r = eps > 0.f ? row_rstd<D, N, R::kLanes>(xa, xb, eps) : 1.f;
+    if (!store) return;
+    float ya[N], yb[N];
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      float p0, p1, q0, q1;
+      fastmath::fmul2(p0, p1, xa[e], xa[e + 1], r, r);
+      fastmath::fmul2(q0, q1, xb[e], xb[e + 1], r, r);
+      fastmath::fmul2(ya[e], ya[e + 1], p0, p1, ac[e], ac[e + 1]);
+      fastmath::ffma2(ya[e], ya[e + 1], q0, q1, bs[e], bs[e + 1], ya[e], ya[e + 1]);
+      fastmath::fmul2(yb[e], yb[e + 1], q0, q1, bc[e], bc[e + 1]);
+      fastmath::ffma2(yb[e], yb[e + 1], p0, p1, as[e], as[e + 1], yb[e], yb[e + 1]);
+    }
+    store_n<T>(out, ya);
+    store_n<T>(out + D / 2, yb);
+  }
+};
+
+// This lane's 16 bytes of either half of a row, zeros when !on.
+template <typename T, int D>
+__device__ __forceinline__ void load_row(const T* p, bool on, uint4& ra, uint4& rb) {
+  ra = rb = make_uint4(0, 0, 0, 0);
+  if (on) {
+    ra = ld16_once(p);
+    rb = ld16_once(p + D / 2);
+  }
+}
+
 // One token's heads of one tensor, normalised (eps > 0) and rotated: row groups g0, g0 + step, ..
-// below `groups` (kRows heads each) of src (heads D apart) to dst (heads `pitch` apart).  The
-// weights are folded into the rotation's factors, so an element costs three multiplications;
+// below `groups` (kRows heads each) of src (heads D apart) to dst (heads `pitch` apart).
 // U groups' loads are issued before the first is used.  place() is called between the first
 // loads and their use: it finds the token's angles, and says whether to store.
 template <typename T, int D, int U, typename Place>
@@ -167,54 +220,26 @@ __device__ __forceinline__ void turn_heads(const T* src, T* dst, int64_t pitch, 
   using R = RowLayout<T, D>;
   constexpr int N = R::N;
   const int lane = threadIdx.x & 31, c = lane % R::kLanes, sub = lane / R::kLanes;
-  float ac[N], bs[N], bc[N], as[N];   // w_a cos, w_b sin, w_b cos, w_a sin
+  Turn<T, D> turn;
   bool first = true, store = true;
   for (int g = g0; g < groups; g += step * U) {
     uint4 ra[U], rb[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = (g + u * step) * R::kRows + sub;
-      ra[u] = rb[u] = make_uint4(0, 0, 0, 0);
-      if (h < heads) {
-        ra[u] = ld16_once(src + (int64_t)h * D + c * N);
-        rb[u] = ld16_once(src + (int64_t)h * D + D / 2 + c * N);
-      }
+      load_row<T, D>(src + (int64_t)h * D + c * N, h < heads, ra[u], rb[u]);
     }
     if (first) {
       float cs[N], sn[N], wa[N], wb[N];
       load_weights<T, D>(w, c, wa, wb);
       store = place(cs, sn);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        ac[e] = wa[e] * cs[e];
-        bs[e] = -wb[e] * sn[e];
-        bc[e] = wb[e] * cs[e];
-        as[e] = wa[e] * sn[e];
-      }
+      turn.set(cs, sn, wa, wb);
       first = false;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = (g + u * step) * R::kRows + sub;
-      float xa[N], xb[N];
-      Vec16<T>::unpack(ra[u], xa);
-      Vec16<T>::unpack(rb[u], xb);
-      const float r = eps > 0.f ? row_rstd<D, N, R::kLanes>(xa, xb, eps) : 1.f;
-      if (h >= heads || !store) continue;
-      float ya[N], yb[N];
-#pragma unroll
-      for (int e = 0; e < N; e += 2) {
-        float p0, p1, q0, q1;
-        fastmath::fmul2(p0, p1, xa[e], xa[e + 1], r, r);
-        fastmath::fmul2(q0, q1, xb[e], xb[e + 1], r, r);
-        fastmath::fmul2(ya[e], ya[e + 1], p0, p1, ac[e], ac[e + 1]);
-        fastmath::ffma2(ya[e], ya[e + 1], q0, q1, bs[e], bs[e + 1], ya[e], ya[e + 1]);
-        fastmath::fmul2(yb[e], yb[e + 1], q0, q1, bc[e], bc[e + 1]);
-        fastmath::ffma2(yb[e], yb[e + 1], p0, p1, as[e], as[e + 1], yb[e], yb[e + 1]);
-      }
-      T* out = dst + (int64_t)h * pitch;
-      store_n<T>(out + c * N, ya);
-      store_n<T>(out + D / 2 + c * N, yb);
+      turn.row(ra[u], rb[u], eps, h < heads && store, dst + (int64_t)h * pitch + c * N);
     }
   }
 }
