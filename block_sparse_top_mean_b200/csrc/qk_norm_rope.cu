@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kWarps = 8;              // of a CTA of the gradient
 constexpr int kUnroll = 4;            // row groups in flight per warp
-constexpr int kFwdCtas = 16;          // forward: warps of an SM, a CTA each (CTAs of 8: 108 us, not 104)
+constexpr int kFwdCtas = 16;          // forward: warps of an SM, a CTA each (8 a CTA: 4% slower)
 constexpr int kFewWarps = 2;          // of a CTA with tokens of few heads
 constexpr int kBwdCtas = 2;           // of the backward kernel on an SM
 
@@ -140,7 +140,30 @@ struct BwdArgs {
   int nq, split_k;                    // n.split: of the queries
 };
 
-template <typename T, typename TG, int D>
+// A lane's part of a row and of its upstream gradient, as loaded.
+template <typename T, typename TG>
+struct GradRow {
+  static constexpr int N = Vec16<T>::N, M = N / Vec16<TG>::N;   // 16-byte loads of a gradient
+  uint4 xa, xb, ga[M], gb[M];
+
+  __device__ __forceinline__ void load(const T* x, const TG* g, int half, bool on) {
+    xa = xb = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < M; ++i) ga[i] = gb[i] = xa;
+    if (!on) return;
+    xa = ld16_once(x);
+    xb = ld16_once(x + half);
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      ga[i] = ld16_once(g + i * (N / M));
+      gb[i] = ld16_once(g + half + i * (N / M));
+    }
+  }
+};
+
+// ONE: a token is one row group (split is 1); its next one's loads are issued before it is worked
+// on (32K tokens of 8 + 1 heads of 64: 58 -> 51 us; 16K of 4 + 4 of 128: 44 -> 33).
+template <typename T, typename TG, int D, bool ONE>
 __global__ void __launch_bounds__(kWarps * 32, kBwdCtas)
 qk_norm_rope_bwd_kernel(const TG* __restrict__ dq, const TG* __restrict__ dk,
                         const T* __restrict__ q, const T* __restrict__ k,
@@ -158,73 +181,92 @@ qk_norm_rope_bwd_kernel(const TG* __restrict__ dq, const TG* __restrict__ dk,
   const int n_cta = keys ? gridDim.x - b.nq : b.nq;
   const int heads = keys ? a.hkv : a.hq, split = keys ? b.split_k : a.split;
   const int64_t stride = keys ? a.ks : a.qs;
-  const T* x0 = keys ? k : q;
-  const TG* y0 = keys ? dk : dq;
-  T* o0 = keys ? dki : dqi;
+  const T* x0 = (keys ? k : q) + c * N;
+  const TG* y0 = (keys ? dk : dq) + c * N;
+  T* o0 = (keys ? dki : dqi) + c * N;
   const int groups = (heads + R::kRows - 1) / R::kRows;
   float wa[N], wb[N], acc_a[N], acc_b[N];
   load_weights<T, D>(keys ? wk : wq, c, wa, wb);
 #pragma unroll
   for (int e = 0; e < N; ++e) acc_a[e] = acc_b[e] = 0.f;
 
-  const int64_t units = a.n_tok * split;
-  for (int64_t unit = (int64_t)cta * kWarps + warp; unit < units;
-       unit += (int64_t)n_cta * kWarps) {
-    const int64_t t = unit / split;
-    if (split == 1 && lane == 0) {
-      prefetch_l2(x0 + t * stride, heads * (int64_t)(D * sizeof(T)));
-      prefetch_l2(y0 + t * heads * D, heads * (int64_t)(D * sizeof(TG)));
+  // one row: dx to out, the products for dw added to (ta, tb)
+  auto row = [&](const GradRow<T, TG>& in, bool on, const float (&cs)[N], const float (&sn)[N],
+                 float (&ta)[N], float (&tb)[N], T* out) {
+    float xa[N], xb[N], ga[N], gb[N];
+    Vec16<T>::unpack(in.xa, xa);
+    Vec16<T>::unpack(in.xb, xb);
+#pragma unroll
+    for (int i = 0; i < GradRow<T, TG>::M; ++i) {
+      Vec16<TG>::unpack(in.ga[i], ga + i * Vec16<TG>::N);
+      Vec16<TG>::unpack(in.gb[i], gb + i * Vec16<TG>::N);
     }
-    const T* xt = x0 + t * stride + c * N;
-    const TG* gt = y0 + t * heads * D + c * N;
-    T* ot = o0 + t * heads * D + c * N;
-    float cs[N], sn[N];
-    lane_cos_sin<N, R::kLanes>(a.tn, token_pos(cu, a.n_docs, t), cs, sn);
-    float ta[N], tb[N];                                   // this token's heads
-#pragma unroll
-    for (int e = 0; e < N; ++e) ta[e] = tb[e] = 0.f;
-    for (int g = (int)(unit - t * split); g < groups; g += split) {
-      const int h = g * R::kRows + sub;
-      const bool on = h < heads;
-      float xa[N], xb[N], ga[N], gb[N];
-      if (on) {
-        load_n<T, N>(xt + h * D, xa);
-        load_n<T, N>(xt + h * D + D / 2, xb);
-        load_n<TG, N>(gt + h * D, ga);
-        load_n<TG, N>(gt + h * D + D / 2, gb);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) xa[e] = xb[e] = ga[e] = gb[e] = 0.f;
-      }
-      const float r = row_rstd<D, N, R::kLanes>(xa, xb, a.eps);
-      float d0 = 0.f, d1 = 0.f;
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float g0 = fmaf(ga[e], cs[e], gb[e] * sn[e]);       // R^T dy of both halves
-        const float g1 = fmaf(gb[e], cs[e], -(ga[e] * sn[e]));
-        xa[e] *= r;
-        xb[e] *= r;
-        ta[e] = fmaf(g0, xa[e], ta[e]);
-        tb[e] = fmaf(g1, xb[e], tb[e]);
-        ga[e] = g0 * wa[e];
-        gb[e] = g1 * wb[e];
-        d0 = fmaf(ga[e], xa[e], d0);
-        d1 = fmaf(gb[e], xb[e], d1);
-      }
-      const float dot = row_sum<R::kLanes>(d0 + d1) * (-1.f / D);
-      if (!on) continue;
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        ga[e] = r * fmaf(xa[e], dot, ga[e]);
-        gb[e] = r * fmaf(xb[e], dot, gb[e]);
-      }
-      store_n<T>(ot + h * D, ga);
-      store_n<T>(ot + h * D + D / 2, gb);
-    }
+    const float r = row_rstd<D, N, R::kLanes>(xa, xb, a.eps);
+    float d0 = 0.f, d1 = 0.f;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      acc_a[e] += ta[e];
-      acc_b[e] += tb[e];
+      const float g0 = fmaf(ga[e], cs[e], gb[e] * sn[e]);         // R^T dy of both halves
+      const float g1 = fmaf(gb[e], cs[e], -(ga[e] * sn[e]));
+      xa[e] *= r;
+      xb[e] *= r;
+      ta[e] = fmaf(g0, xa[e], ta[e]);
+      tb[e] = fmaf(g1, xb[e], tb[e]);
+      ga[e] = g0 * wa[e];
+      gb[e] = g1 * wb[e];
+      d0 = fmaf(ga[e], xa[e], d0);
+      d1 = fmaf(gb[e], xb[e], d1);
+    }
+    const float dot = row_sum<R::kLanes>(d0 + d1) * (-1.f / D);
+    if (!on) return;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      ga[e] = r * fmaf(xa[e], dot, ga[e]);
+      gb[e] = r * fmaf(xb[e], dot, gb[e]);
+    }
+    store_n<T>(out, ga);
+    store_n<T>(out + D / 2, gb);
+  };
+
+  const int64_t units = a.n_tok * split, step = (int64_t)n_cta * kWarps;
+  int64_t unit = (int64_t)cta * kWarps + warp;
+  if (ONE) {
+    const bool there = sub < heads;
+    auto load = [&](int64_t t) {
+      GradRow<T, TG> x;
+      x.load(x0 + t * stride + sub * D, y0 + (t * heads + sub) * D, D / 2, there && t < units);
+      return x;
+    };
+    GradRow<T, TG> cur = load(unit);
+    for (; unit < units; unit += step) {
+      const GradRow<T, TG> next = load(unit + step);
+      float cs[N], sn[N];
+      lane_cos_sin<N, R::kLanes>(a.tn, token_pos(cu, a.n_docs, unit), cs, sn);
+      row(cur, there, cs, sn, acc_a, acc_b, o0 + (unit * heads + sub) * D);
+      cur = next;
+    }
+  } else {
+    for (; unit < units; unit += step) {
+      const int64_t t = unit / split;
+      if (split == 1 && lane == 0) {
+        prefetch_l2(x0 + t * stride, heads * (int64_t)(D * sizeof(T)));
+        prefetch_l2(y0 + t * heads * D, heads * (int64_t)(D * sizeof(TG)));
+      }
+      float cs[N], sn[N];
+      lane_cos_sin<N, R::kLanes>(a.tn, token_pos(cu, a.n_docs, t), cs, sn);
+      float ta[N], tb[N];                                 // this token's heads
+#pragma unroll
+      for (int e = 0; e < N; ++e) ta[e] = tb[e] = 0.f;
+      for (int g = (int)(unit - t * split); g < groups; g += split) {
+        const int h = g * R::kRows + sub;
+        GradRow<T, TG> x;
+        x.load(x0 + t * stride + h * D, y0 + (t * heads + h) * D, D / 2, h < heads);
+        row(x, h < heads, cs, sn, ta, tb, o0 + (t * heads + h) * D);
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        acc_a[e] += ta[e];
+        acc_b[e] += tb[e];
+      }
     }
   }
   if (part == nullptr) return;
@@ -321,7 +363,10 @@ cudaError_t run_bwd(NormArgs& a, const void* dq, const void* dk, const void* q, 
   b.n = a;
   const bool dw = dwq != nullptr || dwk != nullptr;
   const int grid = b.nq + (int)nk;
-  qk_norm_rope_bwd_kernel<T, TG, D><<<grid, kWarps * 32, 0, st>>>(
+  const bool one = a.hq <= kR && a.split == 1;            // (hkv <= hq; then split_k is 1 as well)
+  auto* kernel =
+      one ? qk_norm_rope_bwd_kernel<T, TG, D, true> : qk_norm_rope_bwd_kernel<T, TG, D, false>;
+  kernel<<<grid, kWarps * 32, 0, st>>>(
       (const TG*)dq, (const TG*)dk, (const T*)q, (const T*)k, cu, (const T*)wq, (const T*)wk,
       (T*)dqi, (T*)dki, dw ? part : nullptr, b);
   cudaError_t e = cudaGetLastError();
@@ -377,7 +422,8 @@ cudaError_t launch_qk_norm_rope_bwd(const HeadShape& s, const int32_t* cu, int64
   using B = __nv_bfloat16;
 #define MSA_BWD(T, TG, D) \
   run_bwd<T, TG, D>(a, dq, dk, q, k, cu, wq, wk, dqi, dki, dwq, dwk, part, st)
-  if (s.dtype == MSA_F32) return s.d == 128 ? MSA_BWD(float, float, 128) : MSA_BWD(float, float, 64);
+  if (s.dtype == MSA_F32)
+    return s.d == 128 ? MSA_BWD(float, float, 128) : MSA_BWD(float, float, 64);
   if (grad_dtype == MSA_F32) return s.d == 128 ? MSA_BWD(B, float, 128) : MSA_BWD(B, float, 64);
   return s.d == 128 ? MSA_BWD(B, B, 128) : MSA_BWD(B, B, 64);
 #undef MSA_BWD

@@ -78,6 +78,25 @@ NORM = [  # dtype, d, hq, hkv, cu, base, fused, weighted
 ]
 
 
+# tokens enough for a warp each: every head count's own path, up to and above 32 documents
+LONG = [0, 1, 1, 2500, 4999, 5003]
+MANY = [0, *range(3, 153, 3), 4801]
+NORM += [
+    (torch.bfloat16, 128, 4, 4, LONG, 1e6, True, True),
+    (torch.bfloat16, 128, 8, 1, MANY, 1e6, False, True),
+    (torch.bfloat16, 128, 8, 8, LONG, 1e4, True, True),
+    (torch.bfloat16, 128, 16, 4, MANY, 1e4, True, True),
+    (torch.bfloat16, 128, 12, 6, LONG, 1e4, False, False),
+    (torch.bfloat16, 128, 20, 5, MANY, 1e6, True, True),
+    (torch.bfloat16, 64, 8, 1, MANY, 1e6, True, True),
+    (torch.bfloat16, 64, 24, 12, LONG, 1e6, True, True),
+    (torch.float32, 64, 2, 2, LONG, 1e4, False, True),
+    (torch.float32, 64, 3, 1, MANY, 1e4, True, True),
+    (torch.float32, 128, 8, 4, LONG, 1e4, True, True),
+    (torch.float32, 128, 2, 1, LONG, 1e4, True, True),
+]
+
+
 def _norm_inputs(case, seed):
     dtype, d, hq, hkv, cu, base, fused, weighted = case
     q, k, _ = _qkv(cu[-1], hq, hkv, d, dtype, seed, fused)
@@ -103,7 +122,7 @@ def test_norm_rope_vs_oracle(msa, case):
 @pytest.mark.parametrize("case", NORM, ids=range(len(NORM)))
 def test_norm_rope_bwd_vs_oracle(msa, case, grad):
     dtype, d, hq, hkv, cu, base, fused, weighted = case
-    if cu[-1] > 5000:
+    if cu[-1] > 50000:
         cu = [0, 9, 1033]
         case = (dtype, d, hq, hkv, cu, base, fused, weighted)
     gt = torch.float32 if grad == "f32" else dtype
@@ -149,6 +168,23 @@ def test_norm_rope_bwd_against_differences(msa):
     e[7] = 1.0
     num = (f(q, wq + step * e) - f(q, wq - step * e)) / (2 * step)
     assert abs(num - float(dwq[7])) < 2e-2
+
+
+@pytest.mark.parametrize("heads", [(4, 4), (8, 4), (16, 8), (32, 8)])
+def test_norm_rope_tokens_outside_documents_and_in_place(msa, heads):
+    """Tokens before the first and behind the last document sit at position 0, in every path; in
+    place as out of place."""
+    T = 5000
+    q, k, _ = _qkv(T, *heads, 128, torch.bfloat16, 9)
+    cu = _i32([7, 2000, 4990])
+    a = msa.qk_norm_rope(q, k, cu, 1e4)
+    edge = torch.tensor([*range(7), *range(4990, T)], device="cuda")
+    z = msa.qk_norm_rope(q[edge], k[edge], _i32(list(range(len(edge) + 1))), 1e4)
+    assert torch.equal(a[0][edge], z[0]) and torch.equal(a[1][edge], z[1])
+    mid = msa.qk_norm_rope(q[7:4990], k[7:4990], _i32([0, 1993, 4983]), 1e4)
+    assert torch.equal(a[0][7:4990], mid[0]) and torch.equal(a[1][7:4990], mid[1])
+    msa.qk_norm_rope(q, k, cu, 1e4, out=(q, k))
+    assert torch.equal(q, a[0]) and torch.equal(k, a[1])
 
 
 def test_norm_rope_edges(msa):
