@@ -432,6 +432,45 @@ def test_paged_append_vs_oracle(msa, heads, seqs, base, norm, weighted, queries)
     _close(got[:st.cu[-1]], ref, h * np.abs(ref) + 32 * U * _pair(n))
 
 
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("dtype,d,hq,hkv", [
+    (torch.bfloat16, 128, 4, 4), (torch.bfloat16, 128, 8, 2), (torch.bfloat16, 128, 8, 8),
+    (torch.bfloat16, 128, 12, 3), (torch.bfloat16, 128, 16, 8), (torch.bfloat16, 128, 32, 8),
+    (torch.bfloat16, 64, 8, 1), (torch.float32, 64, 4, 2), (torch.float32, 128, 8, 4),
+    (torch.float32, 128, 0, 3)])
+def test_append_of_many_tokens_is_that_of_a_few(msa, dtype, d, hq, hkv, norm):
+    """A warp a token, or several: bitwise the same pages, queries and errors (40 sequences; one
+    is shorter than its new tokens, one has an entry that is no page, three tokens belong to
+    nobody)."""
+    seqs = [(125, 125 + 31 * i % 200) for i in range(38)] + [(20, 5), (0, 9)]
+    st = Step(dtype, d, max(hq, hkv), hkv, 32, seqs, pad=3, fused=True)
+    st.table[7, 1] = -1
+    st.dev = (_i32(st.table),) + st.dev[1:]
+    pools = [x.nan_to_num_(3.0) for x in (st.kp, st.vp)]
+    wq, wk = _weights(d, dtype, 4) if norm else (None, None)
+    kw = dict(base=1e4 if norm else None, eps=1e-5 if norm else None, wk=wk)
+
+    def append(a, b, kp, vp):
+        x, y = st.cu[a], st.cu[b] + (3 if b == 40 else 0)
+        ws = msa.paged_workspace(st.q, kp, st.dev[1])
+        qs = dict(q=st.q[x:y], wq=wq, out=torch.full((y - x, st.hq, d), 7.0, dtype=dtype,
+                                                     device="cuda")) if hq else {}
+        out = msa.paged_append(st.k[x:y], st.v[x:y], kp, vp, st.dev[0][a:b].contiguous(),
+                               st.dev[1][a:b].contiguous(), st.dev[2][a:b + 1] - x, ws=ws,
+                               **kw, **qs)
+        return out, msa.read_device_error(ws)
+
+    one = [x.clone() for x in pools]
+    out, err = append(0, 40, *one)
+    parts = [append(a, a + 5, *pools) for a in range(0, 40, 5)]
+    assert torch.equal(one[0], pools[0]) and torch.equal(one[1], pools[1])
+    assert err == msa.DEVERR_PAGE_RANGE
+    assert [e for _, e in parts] == [0, err, 0, 0, 0, 0, 0, err]
+    if hq:
+        assert torch.equal(out, torch.cat([o for o, _ in parts]))
+        assert (out[-3:] == 7).all()
+
+
 def test_append_and_norm_rope_agree(msa):
     """The append's keys and queries are bitwise qk_norm_rope's at the same positions."""
     st = Step(torch.bfloat16, 128, 8, 2, 32, [(90, 90), (33, 33)])
