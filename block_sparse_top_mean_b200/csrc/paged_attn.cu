@@ -1,5 +1,7 @@
 // Attention of new tokens over a paged cache: which kernel takes which sequences, and the
 // kernel that joins the parts of items that were cut (see paged.cuh).
+#include <algorithm>
+
 #include "paged.cuh"
 
 namespace msa {
@@ -89,39 +91,76 @@ paged_combine_parts_kernel(PagedParts parts, int rows, T* __restrict__ o,
   store_joined<T, D>(o, lse, part_qrow(rec, row, G, hq), lane, acc, mx, l);
 }
 
-// Many rows, few parts each: a warp a row, which asks for its first two parts (a cut item has
-// two) before it knows their maxima.  (Two and four rows a warp: no faster.)
+// Many rows: a warp a row.  Up to three parts (a cut item has two, and mostly no more) are asked for
+// before their maxima are known; of more, lane i holds the maximum and the weight of part i and
+// the outputs come four at a time (64 tokens over 30000 keys: 36 us, 53 one by one).
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 8)
 paged_combine_rows_kernel(PagedParts parts, int rows, T* __restrict__ o,
                           float* __restrict__ lse, int G, int hq) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, B = 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 rec = parts.rec[blockIdx.x];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = rec.w;
   const int row = blockIdx.y * 8 + warp;
   if (n == 0 || row >= (rec.z >> 1) * G) return;
-  const int64_t at0 = part_slot(rec, 0) * rows + row, at1 = part_slot(rec, 1) * rows + row;
-  const float2 m0 = parts.ml[at0], m1 = parts.ml[at1];
-  float acc[E], y[E];
-  load_part<E>(acc, parts.o + at0 * D + lane * E);
-  load_part<E>(y, parts.o + at1 * D + lane * E);
-  float mx = fmaxf(m0.x, m1.x);
-  for (int i = 2; i < n; ++i) mx = fmaxf(mx, parts.ml[part_slot(rec, i) * rows + row].x);
-  const float ref = mx == -CUDART_INF_F ? 0.f : mx;
-  const float w0 = exp2f(m0.x - ref), w1 = exp2f(m1.x - ref);
-  float l = fmaf(m1.y, w1, m0.y * w0);
+  auto at = [&](int i) -> int64_t { return part_slot(rec, i) * rows + row; };
+  auto part = [&](float (&y)[E], int i) { load_part<E>(y, parts.o + at(i) * D + lane * E); };
+  float acc[E], y[B][E];
+  if (n <= 3) {
+    const float2 m0 = parts.ml[at(0)], m1 = parts.ml[at(1)];
+    part(acc, 0);
+    part(y[0], 1);
+    float2 m2 = make_float2(-CUDART_INF_F, 0.f);
+    if (n == 3) {
+      m2 = parts.ml[at(2)];
+      part(y[1], 2);
+    }
+    const float mx = fmaxf(fmaxf(m0.x, m1.x), m2.x), ref = mx == -CUDART_INF_F ? 0.f : mx;
+    const float w0 = exp2f(m0.x - ref), w1 = exp2f(m1.x - ref), w2 = exp2f(m2.x - ref);
+    float l = fmaf(m1.y, w1, m0.y * w0);
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = fmaf(y[e], w1, acc[e] * w0);
-  for (int i = 2; i < n; ++i) {
-    const int64_t at = part_slot(rec, i) * rows + row;
-    const float2 ml = parts.ml[at];
-    load_part<E>(y, parts.o + at * D + lane * E);
-    const float w = exp2f(ml.x - ref);
-    l = fmaf(ml.y, w, l);
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(y[0][e], w1, acc[e] * w0);
+    if (n == 3) {
+      l = fmaf(m2.y, w2, l);
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(y[e], w, acc[e]);
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(y[1][e], w2, acc[e]);
+    }
+    store_joined<T, D>(o, lse, part_qrow(rec, row, G, hq), lane, acc, mx, l);
+    return;
   }
+  float2 ml = make_float2(-CUDART_INF_F, 0.f);
+  if (lane < n) ml = parts.ml[at(lane)];
+  part(acc, 0);
+  part(y[0], 1);
+  float mx = ml.x;
+  for (int i = 32 + lane; i < n; i += 32) mx = fmaxf(mx, parts.ml[at(i)].x);
+  mx = warp_max(mx);
+  const float ref = mx == -CUDART_INF_F ? 0.f : mx;
+  float w = exp2f(ml.x - ref), l = ml.y * w;
+  const float w0 = __shfl_sync(0xffffffffu, w, 0), w1 = __shfl_sync(0xffffffffu, w, 1);
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = fmaf(y[0][e], w1, acc[e] * w0);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    if (i0 > 0) {                                         // the next 32 parts' weights
+      ml = i0 + lane < n ? parts.ml[at(i0 + lane)] : make_float2(-CUDART_INF_F, 0.f);
+      w = exp2f(ml.x - ref);
+      l = fmaf(ml.y, w, l);
+    }
+    for (int i = i0 == 0 ? 2 : i0; i < min(n, i0 + 32); i += B) {
+#pragma unroll
+      for (int b = 0; b < B; ++b) part(y[b], min(i + b, n - 1));
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const float f = __shfl_sync(0xffffffffu, w, (i + b) & 31);
+        if (i + b < min(n, i0 + 32)) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(y[b][e], f, acc[e]);
+        }
+      }
+    }
+  }
+  l = warp_sum(l);
   store_joined<T, D>(o, lse, part_qrow(rec, row, G, hq), lane, acc, mx, l);
 }
 
@@ -209,10 +248,15 @@ cudaError_t launch_paged_attn(const HeadShape& s, const PagedShape& g, int64_t m
   // 123 on the second, 202 on mma.sync with 64 rows a tile).
   if (rows <= 16) return launch_paged_step(s, a, (int)rows, q, kp, vp, o, lse, parts, err, st);
   // A chunk among generated tokens (the others' average says so): single tokens would fill a few
-  // rows of a 256-row tile each, so they get a launch of their own (48 tokens and a chunk of 1024:
-  // 333 us, 392 us in one launch).
+  // rows of a 256-row tile each, so they get a launch of their own, where the caches are large
+  // enough to pay for it; the host knows what the tables and the pools can hold (48 tokens of 512
+  // keys each, 32 / 8 heads of 128, and a chunk of 1024: 115 us, 107 in one launch; of 2048 keys,
+  // 400 MB: 162 and 163; of 8192: 334 and 396).
   const int small = a.G <= 8 ? 8 : 16;
-  if (g.n_seqs > 1 && a.G <= 16 && (s.n_tok - max_new) * a.G <= 64 * (g.n_seqs - 1)) {
+  const int64_t table_keys = (g.n_seqs - 1) * std::min<int64_t>(g.max_pages * g.page, INT32_MAX);
+  const int64_t keys = std::min(table_keys, g.n_pages * g.page);
+  if (g.n_seqs > 1 && a.G <= 16 && (s.n_tok - max_new) * a.G <= 64 * (g.n_seqs - 1) &&
+      keys * s.hkv * s.d * 4 >= 400000000) {
     PagedAttn b = a;
     b.max_new = small / a.G;
     a.min_new = b.max_new + 1;

@@ -324,6 +324,23 @@ def test_paged_attn_any_hint(msa, hint):
     st.check(*st.attn(msa, max_new=hint))
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (16, 1, 128), (24, 8, 64), (8, 8, 128)])
+def test_paged_attn_chunk_among_single_tokens_of_large_caches(msa, hq, hkv, d):
+    """Pools of more than 400 MB: single tokens and a chunk go to a launch each."""
+    seqs = [(1, 70 * i + 1) for i in range(12)] + [(200, 900), (0, 5), (2, 300),
+                                                   (17 // (hq // hkv), 65)]
+    st = Step(torch.bfloat16, d, hq, hkv, 64, seqs, spare=4000)
+    total = 400000000 // (4 * hkv * d * 64) + 2
+    for name in ("kp", "vp"):
+        big = torch.empty((total, hkv, 64, d), dtype=torch.bfloat16, device="cuda")
+        big[:getattr(st, name).shape[0]] = getattr(st, name)
+        setattr(st, name, big)
+    o = torch.full((st.T, hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((st.T, hq), 7.0, device="cuda")
+    st.attn(msa, out=(o, lse), max_new=200)
+    st.check(o, lse)
+
+
 def test_paged_attn_strided_queries_scale_and_no_lse(msa):
     st = Step(torch.bfloat16, 128, 8, 2, 32, [(70, 150), (1, 40)])
     wide = torch.empty(st.T, 20, 128, dtype=st.dtype, device="cuda")
