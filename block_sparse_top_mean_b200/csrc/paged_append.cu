@@ -199,7 +199,7 @@ cudaError_t run(AppendArgs& a, const void* q, const void* k, const void* v, cons
   constexpr int kR = RowLayout<T, D>::kRows;
   const int gq = (a.hq + kR - 1) / kR, gk = (a.hkv + kR - 1) / kR;
   a.split = head_split(a.n_tok, gq + 2 * gk);
-  if (a.split == 1 && gq <= 4 && gk <= 2) {
+  if (gk <= 2 && (gq <= 2 || (gq <= 4 && a.n_tok >= sm_count()))) {
     const unsigned few = (unsigned)((a.n_tok + kFewWarps - 1) / kFewWarps);
     auto launch = [&](auto* kernel) {
       kernel<<<few, kFewWarps * 32, 0, st>>>((const T*)q, (const T*)k, (const T*)v, (const T*)wq,

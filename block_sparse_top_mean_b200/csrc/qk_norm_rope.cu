@@ -90,7 +90,9 @@ qk_norm_rope_kernel(const T* q, const T* k, const int32_t* __restrict__ cu,
 // Tokens of few heads (up to GQ row groups of queries and GK of keys): all of a token's rows are
 // loaded before its position is looked up, and with fewer registers and CTAs of two warps more
 // tokens are in flight (8 + 1 heads of 64, 32K tokens: 51 -> 22 us; 16 + 4 of 128, 20K: 47 -> 37;
-// two to eight tokens a warp: slower than one).
+// two to eight tokens a warp: slower than one).  It also beats a token's heads dealt to
+// several warps (16 + 4 heads, 500 tokens: 3.9 us, 5.9), but for four groups and fewer
+// tokens than SMs (100: 3.8, 3.6).
 template <typename T, int D, int GQ, int GK>
 __global__ void __launch_bounds__(kFewWarps * 32)
 qk_norm_rope_few_kernel(const T* q, const T* k, const int32_t* __restrict__ cu,
@@ -322,7 +324,7 @@ cudaError_t run_fwd(NormArgs& a, const void* q, const void* k, const int32_t* cu
   constexpr int kR = RowLayout<T, D>::kRows;
   a.split = head_split(a.n_tok, (a.hq + kR - 1) / kR + (a.hkv + kR - 1) / kR);
   const int gq = (a.hq + kR - 1) / kR, gk = (a.hkv + kR - 1) / kR;
-  if (a.split == 1 && gq <= 4 && gk <= 2) {
+  if (gk <= 2 && (gq <= 2 || (gq <= 4 && a.n_tok >= sm_count()))) {
     const unsigned few = (unsigned)((a.n_tok + kFewWarps - 1) / kFewWarps);
     auto launch = [&](auto* kernel) {
       kernel<<<few, kFewWarps * 32, 0, st>>>((const T*)q, (const T*)k, cu, (const T*)wq,
