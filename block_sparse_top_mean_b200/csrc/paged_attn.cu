@@ -91,9 +91,9 @@ paged_combine_parts_kernel(PagedParts parts, int rows, T* __restrict__ o,
   store_joined<T, D>(o, lse, part_qrow(rec, row, G, hq), lane, acc, mx, l);
 }
 
-// Many rows: a warp a row.  Up to three parts (a cut item has two, and mostly no more) are asked for
-// before their maxima are known; of more, lane i holds the maximum and the weight of part i and
-// the outputs come four at a time (64 tokens over 30000 keys: 36 us, 53 one by one).
+// Many rows: a warp a row.  Up to three parts (a cut item has two, and mostly no more) are asked
+// for before their maxima are known; of more, lane i holds the maximum and the weight of part i
+// and the outputs come four at a time (64 tokens over 30000 keys: 36 us, 53 one by one).
 template <typename T, int D>
 __global__ void __launch_bounds__(256, 8)
 paged_combine_rows_kernel(PagedParts parts, int rows, T* __restrict__ o,

@@ -11,8 +11,8 @@
 // rows' loads are issued before the first is used, the token's position is looked up while
 // they are under way, and the token's other rows are asked for to L2 at the warp's start: what
 // a warp has in flight does not end at its registers (32K tokens of 32 + 8 heads of 128, bf16:
-// forward 116 -> 106 us, 6.3 TB/s; gradient 235 -> 214 us, 6.3 TB/s.  With the rows of the
-// warp's next token asked for as well: 278).
+// forward 116 -> 106 us, and 103, 6.5 TB/s, with CTAs of one warp; gradient 235 -> 214 us, 6.3
+// TB/s.  With the rows of the warp's next token asked for as well: 278).
 //
 // dw sums T * heads terms.  A lane adds up the heads of one token first, then the tokens it
 // meets, then lanes, warps and CTAs are joined, each in a fixed order: the sum is the same
