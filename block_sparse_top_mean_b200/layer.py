@@ -256,7 +256,8 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens, max_new
     """Causal attention of packed new tokens q [T, hq, d] over the paged cache that already
     holds their keys and values (see paged_append).  max_new: the most new tokens of any
     sequence as the host knows it (None: unknown); it chooses the kernel, not the result's
-    meaning.  Returns (o [T, hq, d], lse [T, hq] fp32 or None); a token that sees no key gets
+    meaning, and with it how bf16 calls round the softmax's weights before the product with the
+    values: to 2^-17 of each where max_new * hq / hkv <= 16, to 2^-8 above.  Returns (o [T, hq, d], lse [T, hq] fp32 or None); a token that sees no key gets
     o = 0, lse = -inf; packed tokens behind the last sequence are left as they are (`out` may
     pass o and lse)."""
     index, dt = _device("q", q), q.dtype

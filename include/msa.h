@@ -299,9 +299,14 @@ MSA_API msa_status msa_paged_append(const msa_params* p, const msa_paged_cache* 
  * lse = -inf.  Keys past the page table row do not exist; those of a table entry outside
  * [0, n_pages) read as zeros and set MSA_DEVERR_PAGE_RANGE.  Rows of a page behind the last
  * token may hold anything, NaN included; keys and values of the sequence must be finite.
- * max_new: the most new tokens of any sequence, as far as the host knows (0: unknown); it
- * chooses the kernel, not the result's meaning.  A result has the same bits in every run
- * with the same arguments; another max_new may round differently.
+ * max_new: the most new tokens of any sequence, as far as the host knows (0: unknown, then any
+ * may have all T); it chooses the kernel, not the result's meaning.  A result has the same bits
+ * in every run with the same arguments; another max_new rounds differently.  With bf16 tensors
+ * the softmax's weights meet the values as two bf16 terms (2^-17 of each weight) where
+ * max_new * hq / hkv <= 16, and as one (2^-8 of each; typically 1.4 times the error that the
+ * rounding of o itself brings) above that, where the tensor cores' left operand is bf16; single
+ * tokens beside a chunk may be served either way.  Scores, maxima, sums and lse are fp32 in
+ * both, and the sum is that of the unrounded weights.
  * ws: msa_workspace_bytes(p, MSA_OP_PAGED_ATTN, 0); it holds nothing between calls but the
  * error word, and calls that overlap need one each.  hq / hkv up to 64; d 64 or 128. */
 MSA_API msa_status msa_paged_attn_fwd(const msa_params* p, const msa_paged_cache* cache,

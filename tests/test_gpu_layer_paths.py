@@ -1,0 +1,132 @@
+"""Paths of the layer operators that tests/test_gpu_layer.py does not tell apart or does not
+reach: what the weights of each attention kernel carry, head layouts that take the general norm
+and append kernels, wide groups, outputs at odd addresses.  Bounds as derived there (U = 2^-24,
+the half step of an fp32 value; HALF, that of an output's type)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from test_gpu_layer import HALF, U, Step, _close, _np
+from test_gpu_layer import msa  # noqa: F401  (fixture)
+
+gpu = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ the weights' precision
+
+def _bf16(x):
+    """float64 values rounded to bf16 (nearest, ties to even; by way of fp32)."""
+    return torch.tensor(np.asarray(x)).float().bfloat16().double().numpy()
+
+
+def _cancelling(hq, hkv, d, n_new, kv, seed):
+    """One sequence whose outputs cancel: q, k in {-1, 0, 1}, so scores are whole numbers and exact
+    in fp32, and v [kv, hkv, d] of bf16 values whose signs keep the running sum of weight * v of
+    column c, for row c % rows of its KV head, near zero (weights in falling order)."""
+    r = np.random.default_rng(seed)
+    G = hq // hkv
+    q = r.integers(-1, 2, (n_new, hq, d)).astype(np.float64)
+    k = r.integers(-1, 2, (kv, hkv, d)).astype(np.float64)
+    size = _bf16(r.uniform(1, 2, (kv, hkv, d)))
+    v = size.copy()
+    scale = 1.5 / np.sqrt(d)
+    for g in range(hkv):
+        for c in range(d):
+            t, h = divmod(c % (n_new * G), G)
+            see = kv - n_new + t + 1
+            p = np.exp(scale * k[:see, g] @ q[t, g * G + h])
+            total = 0.0
+            for i in np.argsort(-p, kind="stable"):
+                v[i, g, c] = -size[i, g, c] if total > 0 else size[i, g, c]
+                total += p[i] * v[i, g, c]
+    return q, k, v, scale
+
+
+def _attention(q, k, v, scale, round_weights=None):
+    """(o, sum of weight * |v|, targeted) in float64; round_weights: what is planted between the
+    softmax and the product with v (weights relative to the row's largest)."""
+    n, hq, d = q.shape
+    kv, hkv = k.shape[:2]
+    G = hq // hkv
+    o, a = np.zeros((n, hq, d)), np.zeros((n, hq, d))
+    target = np.zeros((n, hq, d), bool)
+    for t in range(n):
+        see = kv - n + t + 1
+        for h in range(hq):
+            x = scale * (k[:see, h // G] @ q[t, h])
+            p = np.exp(x - x.max())
+            w = p if round_weights is None else round_weights(p)
+            o[t, h] = w @ v[:see, h // G] / p.sum()
+            a[t, h] = p @ np.abs(v[:see, h // G]) / p.sum()
+            target[t, h] = np.arange(d) % (n * G) == t * G + h % G
+    return o, a, target
+
+
+CANCEL = [  # hq, hkv, d, new tokens, tokens: up to 16 rows a KV head
+    (8, 2, 128, 1, 97), (8, 1, 64, 1, 33), (16, 1, 128, 1, 230), (8, 2, 128, 4, 65),
+    (2, 2, 64, 1, 120),
+]
+
+
+def _score_error(q, k, scale):
+    """The scores are exact; their scaling and the subtraction of the maximum are off by 2 U each."""
+    k = np.repeat(k, q.shape[1] // k.shape[1], axis=1)
+    return 4 * U * max(1.0, scale * np.abs(np.einsum("thd,khd->tkh", q, k)).max())
+
+
+def _bound(ref, a, q, k, scale, weights):
+    n_keys, e = k.shape[0], _score_error(q, k, scale)
+    return 2.0 ** -8 * np.abs(ref) + a * (2 * e + 2.0 ** -19 + weights + 2 * n_keys * U)
+
+
+@pytest.mark.parametrize("case", CANCEL, ids=range(len(CANCEL)))
+def test_cancelling_values_tell_one_term_from_two(case):
+    """On the CPU: weights of one bf16 term leave the two-term bound at most of the entries whose
+    values cancel; weights of two terms (a rounding of at most 2^-17) stay within it."""
+    hq, hkv, d, n, kv = case
+    q, k, v, scale = _cancelling(*case, seed=5)
+    ref, a, target = _attention(q, k, v, scale)
+    bound = _bound(ref, a, q, k, scale, 2.0 ** -17)
+    one, _, _ = _attention(q, k, v, scale, _bf16)
+    two, _, _ = _attention(q, k, v, scale, lambda p: _bf16(p) + _bf16(p - _bf16(p)))
+    assert (np.abs(one - ref) > bound)[target].mean() > 0.5
+    assert (np.abs(two - ref) <= bound).all()
+
+
+def _cancelling_step(case):
+    hq, hkv, d, n, kv = case
+    q, k, v, scale = _cancelling(*case, seed=5)
+    st = Step(torch.bfloat16, d, hq, hkv, 32, [(n, kv)])
+    st.q = torch.tensor(q, device="cuda").bfloat16()
+    for pool, x in ((st.kp, k), (st.vp, v)):
+        pages = torch.tensor(st.table[0], device="cuda").long()
+        x = torch.tensor(x, device="cuda").bfloat16()
+        for p in range(kv):
+            pool[pages[p // 32], :, p % 32] = x[p]
+    return st, q, k, v, scale
+
+
+@gpu
+@pytest.mark.parametrize("case", CANCEL, ids=range(len(CANCEL)))
+def test_weights_of_few_rows_carry_two_terms(msa, case):  # noqa: F811
+    """Up to 16 rows of a KV head: the weights meet V with 2^-17, not with a bf16's 2^-8."""
+    hq, hkv, d, n, kv = case
+    st, q, k, v, scale = _cancelling_step(case)
+    ref, a, _ = _attention(q, k, v, scale)
+    o, _ = st.attn(msa, scale=scale, max_new=n)
+    _close(o, ref, _bound(ref, a, q, k, scale, 2.0 ** -17))
+
+
+@gpu
+@pytest.mark.parametrize("case", [(8, 1, 128, 40, 97), (16, 4, 64, 9, 230), (32, 1, 128, 1, 65)])
+def test_weights_of_many_rows_are_rounded_once(msa, case):  # noqa: F811
+    """Above 16 rows: weights of one bf16 term, 2^-8 of each, while the sum they are divided by,
+    and lse, keep the unrounded ones."""
+    hq, hkv, d, n, kv = case
+    st, q, k, v, scale = _cancelling_step(case)
+    ref, a, _ = _attention(q, k, v, scale)
+    o, lse = st.attn(msa, scale=scale, max_new=n)
+    _close(o, ref, _bound(ref, a, q, k, scale, 2.0 ** -8))
+    rl = oracle.paged_attention(q, _np(st.kp), _np(st.vp), st.table, st.kv, st.cu, 32, scale)[1]
+    _close(lse, rl, _score_error(q, k, scale) + 2.0 ** -20 + kv * U + 4 * U * np.abs(rl))
