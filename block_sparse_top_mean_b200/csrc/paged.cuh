@@ -100,6 +100,11 @@ constexpr int kPagedCtas = 160;       // most SMs a schedule uses (a B200 has 14
 constexpr int kPagedRecs = 2 * kPagedCtas;       // most CTAs: two an SM with row tiles of up to 64
 constexpr int kPagedMaxRows = 256;    // rows of the largest row tile (one CTA an SM)
 
+// A build that tests how the kernels give up loses this copy of every CTA's stream.
+#ifndef MSA_LOSE_COPY
+#define MSA_LOSE_COPY -1
+#endif
+
 // Workspace body: records, then (maximum, sum) and outputs of the parts.  CTA c's parts: 2c
 // (its first item) and 2c + 1 (its last, when that is another).  Sized for one CTA an SM with
 // row tiles of kPagedMaxRows; smaller row tiles leave room for more CTAs.

@@ -51,7 +51,7 @@ template <int D> constexpr int kUnits = D == 128 ? 5 : 10;   // 160 KB
 template <int D>
 struct __align__(16) Shared {
   uint64_t kv_full[kUnits<D>], kv_empty[kUnits<D>];
-  uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_full[2], o_empty[2];
+  uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_full[2], o_empty[2], idle;
   uint32_t tmem;
   int abort;
   PlanSmem plan;
@@ -69,7 +69,7 @@ __device__ __forceinline__ bool wait(Shared<D>& sm, uint64_t* bar, uint32_t pari
   bool ok = mbar_try_wait(bar, parity);
   if (__all_sync(0xffffffffu, ok)) return true;
   const long long t0 = clock64();
-  while (!ok && *(volatile int*)&sm.abort == 0 && clock64() - t0 < 4000000000LL)
+  while (!ok && *(volatile int*)&sm.abort == 0 && clock64() - t0 < MSA_WAIT_CLOCKS)
     ok = mbar_try_wait(bar, parity);
   if (__all_sync(0xffffffffu, ok)) return true;
   if (threadIdx.x % 32 == 0) give_up(sm, err);
@@ -199,6 +199,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
     }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.idle, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sm.s_full[x], 1);
       mbar_init(&sm.p_full[x][0], kHalfRows);
@@ -257,7 +258,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
           }
           if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[u], (uint32_t)(n * box * D * 2));
           __syncwarp();
-          if (mine) {
+          if (mine && units != MSA_LOSE_COPY) {
 #pragma unroll
             for (int h = 0; h < DH; ++h)
               tma_load_2d(ring + u * kUnit<D> + h * kHalf + lane * box * 128, v ? &tm_v : &tm_k,
@@ -383,6 +384,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
       }
       ++item;
     } while (ok && run_next<KT>(a, r));
+    // No product may read shared memory, write TMEM or arrive at a barrier after the CTA ends: when
+    // a wait ran out, nobody else has waited for those under way.
+    if (elect_one()) umma_commit(&sm.idle);
+    __syncwarp();
+    mbar_wait_warp(&sm.idle, 0);
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");

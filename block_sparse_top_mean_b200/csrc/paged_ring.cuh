@@ -46,7 +46,7 @@ __device__ __forceinline__ bool ring_wait(Ring<ST, W>& sm, uint64_t* bar, uint32
   bool ok = mbar_try_wait(bar, parity);
   if (__all_sync(0xffffffffu, ok)) return true;
   const long long t0 = clock64();
-  while (!ok && *(volatile int*)&sm.abort == 0 && clock64() - t0 < 4000000000LL)
+  while (!ok && *(volatile int*)&sm.abort == 0 && clock64() - t0 < MSA_WAIT_CLOCKS)
     ok = mbar_try_wait(bar, parity);
   if (__all_sync(0xffffffffu, ok)) return true;
   if (threadIdx.x % 32 == 0) ring_fail(sm, err);

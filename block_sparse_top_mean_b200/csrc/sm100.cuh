@@ -18,6 +18,12 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// How long a bounded wait lasts, in SM clocks (~2 s); a build that tests how kernels give up
+// shortens it.
+#ifndef MSA_WAIT_CLOCKS
+#define MSA_WAIT_CLOCKS 4000000000LL
+#endif
+
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count)
@@ -48,7 +54,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 // Waits for the phase with the given parity to complete; gives up after ~`cycles` SM
 // clocks and returns false (the caller flags the error and leaves).
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
-                                          long long cycles = 4000000000LL) {
+                                          long long cycles = MSA_WAIT_CLOCKS) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
