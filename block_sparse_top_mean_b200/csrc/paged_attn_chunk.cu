@@ -288,11 +288,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
       }
     } while (ok && run_next<KT>(a, r));
-    if (!ok) {                                            // no copy may land after the CTA ends
-      for (int s = units > NU ? units - NU : 0; s < units; ++s)
-        mbar_wait_warp(&sm.kv_full[s % NU], (uint32_t)(s / NU) & 1);
-      if (item > 0) mbar_wait_warp(&sm.q_full, (uint32_t)(item - 1) & 1);
-    }
+    // No copy may land after the CTA ends, whoever gave up: the last ones are waited for.
+    for (int s = units > NU ? units - NU : 0; s < units; ++s)
+      mbar_wait_warp(&sm.kv_full[s % NU], (uint32_t)(s / NU) & 1);
+    if (item > 0) mbar_wait_warp(&sm.q_full, (uint32_t)(item - 1) & 1);
   } else if (warp == kIssuer) {
     // ---------------------------------------------------------------- issuer
     const uint32_t id_s = idesc_bf16(128, KT, 0, 0), id_o = idesc_bf16(128, D, 0, 1);

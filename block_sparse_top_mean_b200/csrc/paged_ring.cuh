@@ -96,7 +96,7 @@ __device__ __forceinline__ void produce(const CUtensorMap& tm_k, const CUtensorM
       const int n = __popc(__ballot_sync(0xffffffffu, mine));
       if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], (uint32_t)(n * box * D * E * 2));
       __syncwarp();
-      if (mine) {
+      if (mine && step != MSA_LOSE_COPY) {
         unsigned char* dst = ring + st * kStageBytes<D, E> + lane * box * 128;
 #pragma unroll
         for (int h = 0; h < kSlices<D, E>; ++h) {
@@ -111,9 +111,10 @@ __device__ __forceinline__ void produce(const CUtensorMap& tm_k, const CUtensorM
       }
     }
   } while (ok && run_next<KT>(a, r));
-  if (!ok)                                                // no copy may land after the CTA ends
-    for (int s = step > ST ? step - ST : 0; s < step; ++s)
-      mbar_wait_warp(&sm.full[s % ST], (uint32_t)(s / ST) & 1);
+  // No copy may land after the CTA ends, whoever gave up (in a run shorter than the ring the
+  // consumers alone may): the last one of every stage is waited for.
+  for (int s = step > ST ? step - ST : 0; s < step; ++s)
+    mbar_wait_warp(&sm.full[s % ST], (uint32_t)(s / ST) & 1);
 }
 
 // Set-up: barriers (readers: warps that read a stage), this CTA's record, the run.
