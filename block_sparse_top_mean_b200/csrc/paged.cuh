@@ -23,9 +23,8 @@
 
 #include <math_constants.h>
 
-#include <atomic>
-
 #include "common.cuh"
+#include "device_once.cuh"
 
 namespace msa {
 
@@ -72,7 +71,7 @@ size_t paged_attn_ws_bytes(const HeadShape& s);
 int paged_grid();                     // CTAs of a schedule: one an SM
 // Raises a kernel's shared memory limit on the current device, once (done: the kernel's own
 // record of the devices where that happened).
-cudaError_t raise_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>* done);
+cudaError_t raise_smem(const void* kernel, size_t bytes, DeviceOnce* done);
 // Each kernel takes the sequences with a.min_new .. a.max_new new tokens, whatever their rows.
 // rows: the row tile asked for (at least G).  step: bf16, up to 16 rows; f32: fp32; chunk: bf16
 // on the tensor cores, row tiles of 2 x 128 rows.

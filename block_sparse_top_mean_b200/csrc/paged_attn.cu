@@ -200,14 +200,12 @@ size_t paged_attn_ws_bytes(const HeadShape& s) {
          (size_t)2 * kPagedCtas * kPagedMaxRows * (sizeof(float2) + s.d * sizeof(float));
 }
 
-cudaError_t raise_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>* done) {
+cudaError_t raise_smem(const void* kernel, size_t bytes, DeviceOnce* done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (dev < 64 && (done->load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  if (e != cudaSuccess || done->done(dev)) return e;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  if (e == cudaSuccess) done->mark(dev);
   return e;
 }
 

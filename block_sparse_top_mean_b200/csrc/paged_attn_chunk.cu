@@ -493,7 +493,7 @@ cudaError_t run(PagedAttn& a, const HeadShape& s, const void* q, const void* kp,
       !make_bf16_2d_map(&mk, kp, pool, D, box) || !make_bf16_2d_map(&mv, vp, pool, D, box))
     return cudaErrorInvalidValue;
   const size_t smem = 1024 + 2 * (D / 64) * kHalf + kUnits<D> * kUnit<D> + sizeof(Shared<D>);
-  static std::atomic<uint64_t> done{0};
+  static DeviceOnce done;
   cudaError_t e = raise_smem((const void*)paged_chunk_kernel<D>, smem, &done);
   if (e != cudaSuccess) return e;
   const int grid = paged_grid();

@@ -455,7 +455,7 @@ paged_rows32_kernel(const __grid_constant__ CUtensorMap tm_k,
 }
 
 template <typename K>
-cudaError_t run(K kernel, std::atomic<uint64_t>* done, int rows, int threads, int grid,
+cudaError_t run(K kernel, DeviceOnce* done, int rows, int threads, int grid,
                 size_t smem, PagedAttn& a, const HeadShape& s, const void* q, const void* kp,
                 const void* vp, void* o, float* lse, const PagedParts& parts, int* err,
                 cudaStream_t st) {
@@ -475,7 +475,7 @@ template <int D>
 cudaError_t run_rows(int rows, PagedAttn& a, const HeadShape& s, const void* q, const void* kp,
                      const void* vp, void* o, float* lse, const PagedParts& parts, int* err,
                      cudaStream_t st) {
-  static std::atomic<uint64_t> done[3];
+  static DeviceOnce done[3];
   constexpr size_t step = ring_bytes<D, 4, kStepStages<D>, kStepWarps>();
   if (rows <= 4)
     return run(paged_step32_kernel<D, 1>, &done[0], 4, kStepThreads, paged_grid(),

@@ -324,7 +324,7 @@ cudaError_t run(PagedAttn& a, const HeadShape& s, const void* q, const void* kp,
   if (!pool_maps(a, s, kp, vp, &mk, &mv, &box)) return cudaErrorInvalidValue;
   constexpr size_t smem = ring_bytes<D, 2, kStages<D>, kConsumers>() + sizeof(Join<D, 8 * NQ>);
   static_assert(kCtas * (smem + 1024) <= 233472, "228 KB an SM");
-  static std::atomic<uint64_t> done{0};
+  static DeviceOnce done;
   cudaError_t e = raise_smem((const void*)paged_step_kernel<D, NQ>, smem, &done);
   if (e != cudaSuccess) return e;
   const int grid = kCtas * paged_grid();
