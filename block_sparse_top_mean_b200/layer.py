@@ -19,6 +19,7 @@ from ._lib import MSA_BF16, MSA_F32, MsaError, MsaParams
 
 _DT = {torch.float32: MSA_F32, torch.bfloat16: MSA_BF16}
 _I32, _F32 = torch.int32, torch.float32
+_MIN_EPS = 2.0 ** -126             # the smallest normal fp32 number
 _fns = {}
 # The images of msa_params and msa_paged_cache, passed by address: packing one takes a quarter of
 # the time of a ctypes structure (0.12 us, 0.56).
@@ -210,6 +211,17 @@ def paged_workspace(q, k_pages, kv_lens):
     return _workspace(p, _lib.OP_PAGED_ATTN, q.device)
 
 
+def _append_eps(eps, wq, wk):
+    """The C entry's eps: 0 stands for no norm there, so none may round to it."""
+    if eps is None:
+        if wq is not None or wk is not None:
+            _fail("wq and wk need eps")
+        return 0.0
+    if not eps >= _MIN_EPS:
+        _fail("eps must be positive, 2^-126 at least (None: no norm)")
+    return eps
+
+
 def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None, base=None,
                  wq=None, wk=None, eps=None, ws=None, out=None):
     """Appends packed new tokens k, v [T, hkv, d] to the paged cache k_pages, v_pages
@@ -233,12 +245,7 @@ def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, q=None
         qp, op = q.data_ptr(), qo.data_ptr()
     elif out is not None or wq is not None:
         _fail("out and wq are for a call with q")
-    if eps is None:
-        if wq is not None or wk is not None:
-            _fail("wq and wk need eps")
-        eps = 0.0
-    elif not eps > 0:
-        _fail("eps must be positive (None: no norm)")
+    eps = _append_eps(eps, wq, wk)
     if base is None:
         base = 0.0
     elif not base > 1:
