@@ -90,8 +90,8 @@ paged_append_kernel(const T* q, const T* k, const T* v, const T* __restrict__ wq
       sn[e] = a.rotate ? sn0[e] : 0.f;
     }
   };
-  turn_heads<T, D, kUnroll>(q + t * a.qs, qo + t * a.hq * D, D, a.hq, wq, a.eps, part, a.split, gq,
-                            [&](float (&cs)[N], float (&sn)[N]) {
+  turn_heads<T, D, kUnroll>(q + t * a.qs, qo + t * a.hq * D, D, a.hq, wq, a.eps, a.rotate, part,
+                            a.split, gq, [&](float (&cs)[N], float (&sn)[N]) {
                               place(cs, sn);
                               return at.mine;
                             });
@@ -115,7 +115,7 @@ paged_append_kernel(const T* q, const T* k, const T* v, const T* __restrict__ wq
   if (g0 < gk) {
     find();
     turn_heads<T, D, 2>(k + t * a.ks, kp + max(at.slot, (int64_t)0) * D, a.g.page * D, a.hkv, wk,
-                        a.eps, g0, a.split, gk, [&](float (&cs)[N], float (&sn)[N]) {
+                        a.eps, a.rotate, g0, a.split, gk, [&](float (&cs)[N], float (&sn)[N]) {
                           place(cs, sn);
                           return at.slot >= 0;
                         });
@@ -170,27 +170,32 @@ paged_append_few_kernel(const T* q, const T* k, const T* v, const T* __restrict_
   }
   if (a.rotate) lane_cos_sin<N, R::kLanes>(a.tn, at.pos, cs, sn);
   Turn<T, D> turn;
-  if (a.hq > 0) {
-    load_weights<T, D>(wq, c, wa, wb);
+  auto rows = [&](auto rot) {
+    if (a.hq > 0) {
+      load_weights<T, D>(wq, c, wa, wb);
+      turn.set(cs, sn, wa, wb);
+#pragma unroll
+      for (int g = 0; g < GQ; ++g) {
+        const int h = g * R::kRows + sub;
+        turn.template row<rot.value>(qa[g], qb[g], a.eps, h < a.hq,
+                                     qo + (t * a.hq + h) * D + c * N);
+      }
+    }
+    if (at.slot < 0) return;
+    load_weights<T, D>(wk, c, wa, wb);
     turn.set(cs, sn, wa, wb);
 #pragma unroll
-    for (int g = 0; g < GQ; ++g) {
+    for (int g = 0; g < GK; ++g) {
       const int h = g * R::kRows + sub;
-      turn.row(qa[g], qb[g], a.eps, h < a.hq, qo + (t * a.hq + h) * D + c * N);
+      const int64_t row = (at.slot + (int64_t)h * a.g.page) * D + c * N;
+      turn.template row<rot.value>(ka[g], kb[g], a.eps, h < a.hkv, kp + row);
+      if (h >= a.hkv) continue;
+      *reinterpret_cast<uint4*>(vp + row) = va[g];
+      *reinterpret_cast<uint4*>(vp + row + D / 2) = vb[g];
     }
-  }
-  if (at.slot < 0) return;
-  load_weights<T, D>(wk, c, wa, wb);
-  turn.set(cs, sn, wa, wb);
-#pragma unroll
-  for (int g = 0; g < GK; ++g) {
-    const int h = g * R::kRows + sub;
-    const int64_t row = (at.slot + (int64_t)h * a.g.page) * D + c * N;
-    turn.row(ka[g], kb[g], a.eps, h < a.hkv, kp + row);
-    if (h >= a.hkv) continue;
-    *reinterpret_cast<uint4*>(vp + row) = va[g];
-    *reinterpret_cast<uint4*>(vp + row + D / 2) = vb[g];
-  }
+  };
+  if (a.rotate) rows(std::true_type{});
+  else rows(std::false_type{});
 }
 
 template <typename T, int D>

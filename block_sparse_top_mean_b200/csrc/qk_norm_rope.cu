@@ -81,9 +81,9 @@ qk_norm_rope_kernel(const T* q, const T* k, const int32_t* __restrict__ cu,
     for (int e = 0; e < N; ++e) { cs[e] = cs0[e]; sn[e] = sn0[e]; }
     return true;
   };
-  turn_heads<T, D, kUnroll>(q + t * a.qs, qo + t * a.hq * D, D, a.hq, wq, a.eps, part, a.split, gq,
-                            place);
-  turn_heads<T, D, 2>(k + t * a.ks, ko + t * a.hkv * D, D, a.hkv, wk, a.eps,
+  turn_heads<T, D, kUnroll>(q + t * a.qs, qo + t * a.hq * D, D, a.hq, wq, a.eps, true, part,
+                            a.split, gq, place);
+  turn_heads<T, D, 2>(k + t * a.ks, ko + t * a.hkv * D, D, a.hkv, wk, a.eps, true,
                       first_group(gq, part, a.split) - gq, a.split, gk, place);
 }
 
@@ -122,14 +122,14 @@ qk_norm_rope_few_kernel(const T* q, const T* k, const int32_t* __restrict__ cu,
 #pragma unroll
   for (int g = 0; g < GQ; ++g) {
     const int h = g * R::kRows + sub;
-    turn.row(qa[g], qb[g], a.eps, h < a.hq, qo + (t * a.hq + h) * D + c * N);
+    turn.template row<true>(qa[g], qb[g], a.eps, h < a.hq, qo + (t * a.hq + h) * D + c * N);
   }
   load_weights<T, D>(wk, c, wa, wb);
   turn.set(cs, sn, wa, wb);
 #pragma unroll
   for (int g = 0; g < GK; ++g) {
     const int h = g * R::kRows + sub;
-    turn.row(ka[g], kb[g], a.eps, h < a.hkv, ko + (t * a.hkv + h) * D + c * N);
+    turn.template row<true>(ka[g], kb[g], a.eps, h < a.hkv, ko + (t * a.hkv + h) * D + c * N);
   }
 }
 

@@ -130,3 +130,35 @@ def test_weights_of_many_rows_are_rounded_once(msa, case):  # noqa: F811
     _close(o, ref, _bound(ref, a, q, k, scale, 2.0 ** -8))
     rl = oracle.paged_attention(q, _np(st.kp), _np(st.vp), st.table, st.kv, st.cu, 32, scale)[1]
     _close(lse, rl, _score_error(q, k, scale) + 2.0 ** -20 + kv * U + 4 * U * np.abs(rl))
+
+
+# ------------------------------------------------------------------ append without a rotation
+
+@gpu
+@pytest.mark.parametrize("dtype,hq,hkv", [
+    (torch.bfloat16, 4, 2), (torch.bfloat16, 32, 8), (torch.float32, 2, 1), (torch.float32, 16, 4)])
+@pytest.mark.parametrize("tokens", [5, 1300])
+def test_append_without_rotation_keeps_elements_apart(msa, dtype, hq, hkv, tokens):  # noqa: F811
+    """Neither norm nor rotation: a copy, infinities, NaN and zeros' signs included.  A norm alone: an
+    infinite element makes the others of its row zero, and none of them NaN."""
+    st = Step(dtype, 128, hq, hkv, 32, [(tokens, tokens)])
+    for x in (st.q, st.k):
+        x[1, :, 3], x[2, :, 70], x[3, :, 5] = float("inf"), -float("inf"), float("nan")
+        x[4, :, :70] = -0.0
+    bits = torch.int16 if dtype == torch.bfloat16 else torch.int32
+
+    def rows(pool):
+        pages = torch.tensor(st.table[0], device="cuda").long()
+        return pool[pages[pages >= 0]].transpose(1, 2).reshape(-1, hkv, 128)[:tokens]
+
+    q = msa.paged_append(st.k, st.v, st.kp, st.vp, *st.dev, q=st.q)
+    for got, want in ((q, st.q), (rows(st.kp), st.k), (rows(st.vp), st.v)):
+        nan = want.isnan()
+        assert torch.equal(got.isnan(), nan)
+        assert torch.equal(got.contiguous().view(bits)[~nan], want.contiguous().view(bits)[~nan])
+    q = msa.paged_append(st.k, st.v, st.kp, st.vp, *st.dev, q=st.q, eps=1e-6)
+    for got in (q, rows(st.kp)):
+        for t, c in ((1, 3), (2, 70)):
+            assert got[t, :, c].isnan().all()
+            assert (got[t, :, :c] == 0).all() and (got[t, :, c + 1:] == 0).all()
+        assert (got[4, :, :70] == 0).all() and got[4].isfinite().all()
