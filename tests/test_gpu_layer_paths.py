@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import oracle
+import test_gpu_layer as base
 from test_gpu_layer import HALF, U, Step, _close, _np
 from test_gpu_layer import msa  # noqa: F401  (fixture)
 
@@ -162,3 +163,84 @@ def test_append_without_rotation_keeps_elements_apart(msa, dtype, hq, hkv, token
             assert got[t, :, c].isnan().all()
             assert (got[t, :, :c] == 0).all() and (got[t, :, c + 1:] == 0).all()
         assert (got[4, :, :70] == 0).all() and got[4].isfinite().all()
+
+
+# ------------------------------------------------------------------ the general kernels
+
+# The norm and the append give tokens of few row groups (a group: 32 / (d sizeof / 32) heads) kernels
+# of their own; these layouts have more than four groups of queries or more than two of keys.
+GENERAL = [  # dtype, d, hq, hkv
+    (torch.float32, 128, 32, 8), (torch.float32, 128, 6, 6), (torch.float32, 128, 16, 2),
+    (torch.float32, 64, 32, 8), (torch.float32, 64, 17, 17), (torch.bfloat16, 64, 64, 8),
+    (torch.bfloat16, 64, 24, 24), (torch.bfloat16, 64, 33, 11),
+]
+
+
+@gpu
+@pytest.mark.parametrize("cu", [[0, 3, 3, 50], base.LONG], ids=["several_warps", "one_warp"])
+@pytest.mark.parametrize("heads", GENERAL, ids=range(len(GENERAL)))
+def test_norm_rope_general_kernel(msa, heads, cu):  # noqa: F811
+    """Forward and gradient, a token's heads dealt to several warps or all one warp's."""
+    base.test_norm_rope_vs_oracle(msa, (*heads, cu, 1e6, True, True))
+    base.test_norm_rope_vs_oracle(msa, (*heads, cu, 1e4, False, False))
+    base.test_norm_rope_bwd_vs_oracle(msa, (*heads, cu, 1e6, True, True), "same")
+    base.test_norm_rope_bwd_vs_oracle(msa, (*heads, cu, 1e4, False, False), "f32")
+
+
+@gpu
+@pytest.mark.parametrize("seqs", ["chunks", "steps", "empties", "many"])
+@pytest.mark.parametrize("heads", GENERAL, ids=range(len(GENERAL)))
+def test_append_general_kernel(msa, monkeypatch, heads, seqs):  # noqa: F811
+    monkeypatch.setitem(base.HEADS, "x", (*heads, 48))
+    monkeypatch.setitem(base.SEQS, "many", [(700, 700), (600, 900), (1, 5)])
+    base.test_paged_append_vs_oracle(msa, "x", seqs, 1e6, True, True, True)
+    base.test_paged_append_vs_oracle(msa, "x", seqs, 1e4, False, False, True)
+
+
+@gpu
+@pytest.mark.parametrize("heads", GENERAL, ids=range(len(GENERAL)))
+def test_append_general_kernel_of_many_tokens_is_that_of_a_few(msa, heads):  # noqa: F811
+    base.test_append_of_many_tokens_is_that_of_a_few(msa, *heads, True)
+
+
+# ------------------------------------------------------------------ wide groups, odd addresses
+
+WIDE = {   # dtype, d, hq, hkv, page: up to 64 query heads of a KV head
+    "bf16_g64": (torch.bfloat16, 128, 64, 1, 64),
+    "bf16_g64_d64": (torch.bfloat16, 64, 128, 2, 16),
+    "bf16_g17": (torch.bfloat16, 128, 34, 2, 48),
+    "bf16_g33_d64": (torch.bfloat16, 64, 33, 1, 128),
+    "bf16_g63": (torch.bfloat16, 128, 63, 1, 80),
+    "f32_g64": (torch.float32, 128, 64, 1, 64),
+    "f32_g33_d64": (torch.float32, 64, 33, 1, 32),
+    "f32_g16": (torch.float32, 128, 16, 1, 16),
+}
+
+
+@gpu
+@pytest.mark.parametrize("seqs", base.SEQS)
+@pytest.mark.parametrize("heads", WIDE)
+def test_paged_attn_wide_groups(msa, monkeypatch, heads, seqs):  # noqa: F811
+    monkeypatch.setitem(base.HEADS, heads, WIDE[heads])
+    base.test_paged_attn_vs_oracle(msa, heads, seqs)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,hint", [(64, None), (128, None), (128, 1), (64, 2)])
+def test_paged_attn_output_at_any_16_bytes(msa, dtype, d, hint):  # noqa: F811
+    """Outputs that start 16 bytes behind a 32-byte boundary: the same bits, nothing around them
+    touched."""
+    st = Step(dtype, d, 8, 2, 64, [(70, 150), (1, 40), (3, 9)])
+    want, wl = st.attn(msa, max_new=hint)
+    step, n = 16 // want.element_size(), want.numel()
+    room = torch.full((n + 4 * step,), 7.0, dtype=dtype, device="cuda")
+    lroom = torch.full((wl.numel() + 2,), 7.0, device="cuda")
+    o, lse = room[step:step + n].view(want.shape), lroom[1:-1].view(wl.shape)
+    assert o.data_ptr() % 32 == 16
+    st.attn(msa, out=(o, lse), max_new=hint)
+    assert torch.equal(o, want) and torch.equal(lse, wl)
+    assert (room[:step] == 7).all() and (room[step + n:] == 7).all()
+    assert lroom[0] == 7 and lroom[-1] == 7
+    with pytest.raises(msa.MsaError):
+        st.attn(msa, out=(room[1:1 + n].view(want.shape), lse), max_new=hint)
