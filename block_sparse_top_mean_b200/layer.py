@@ -264,9 +264,18 @@ def paged_attn_fwd(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens, max_new
     holds their keys and values (see paged_append).  max_new: the most new tokens of any
     sequence as the host knows it (None: unknown); it chooses the kernel, not the result's
     meaning, and with it how bf16 calls round the softmax's weights before the product with the
-    values: to 2^-17 of each where max_new * hq / hkv <= 16, to 2^-8 above.  Returns (o [T, hq, d], lse [T, hq] fp32 or None); a token that sees no key gets
-    o = 0, lse = -inf; packed tokens behind the last sequence are left as they are (`out` may
-    pass o and lse)."""
+    values: to 2^-17 of each where max_new * hq / hkv <= 16, to 2^-8 above.  Returns
+    (o [T, hq, d], lse [T, hq] fp32 or None); a token that sees no key gets o = 0, lse = -inf;
+    packed tokens behind the last sequence are left as they are (`out` may pass o and lse).
+
+    What goes wrong on the device is reported in ws (read_device_error): DEVERR_PAGE_RANGE for a
+    table entry that is no page (its keys and values count as zeros), DEVERR_TIMEOUT for a wait
+    that ran out (results are then incomplete).  Without ws the call makes itself a workspace
+    (43 MB at d = 128) that ends with it, and nothing reports either.
+
+    Pass max_new where all sequences have few new tokens: a batch of single tokens whose hint
+    is left out counts as one that may hold a chunk (48 sequences of up to 16384 keys 71 us,
+    49 with it; 64 of 512 44 and 32; 32 / 8 heads of 128)."""
     index, dt = _device("q", q), q.dtype
     c, n, hkv, page, d = _cache(k_pages, v_pages, page_table, kv_lens, cu_seqlens, dt, index)
     if q.dim() != 3:
