@@ -140,13 +140,6 @@ __device__ __forceinline__ uint4 ld16_once(const void* p) {
                : "l"(p));
   return r;
 }
-// Loads N elements of T at p into fp32 (the 8 fp32 gradients of a bf16 chunk take two loads).
-template <typename T, int N>
-__device__ __forceinline__ void load_n(const T* p, float* f) {
-  constexpr int M = Vec16<T>::N;
-#pragma unroll
-  for (int i = 0; i < N; i += M) Vec16<T>::unpack(ld16_once(p + i), f + i);
-}
 // Rounds N = Vec16<T>::N values to T and stores them as 16 bytes.
 template <typename T>
 __device__ __forceinline__ void store_n(T* p, const float* f) {
