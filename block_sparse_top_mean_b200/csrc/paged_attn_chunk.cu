@@ -13,13 +13,14 @@
 //                   product that reads P_X from the same columns;
 //   two warpgroups  the softmax of one half each, one thread a row: scores from TMEM, base-2
 //                   exponentials, P back to TMEM as bf16 (rounded once, 2^-8 of each weight: the
-//                   tensor core takes no wider left operand beside a bf16 V) in two parts, so the
+//                   tensor core takes no wider left operand beside a bf16 V; a second bf16 term,
+//                   2^-17, was measured: the prompt below 455 -> 627 us) in two parts, so the
 //                   product with V starts at half of them.  The exponent reference moves only
 //                   when a row's maximum outgrows it by 2^8, so O is rarely rescaled.
 // What bounds it: softmax and products in turn, 2.0 us a tile of 256 x 128 at d = 128 (1.64 with
-// the softmax left out).  2048 tokens over 30720 keys, 32 / 8 heads: 871 us, 1223 TFLOP/s; a
-// prompt of 8192: 459 us; four ragged chunks over 12000 keys in pages of 16: 84 us, of which
-// about 4 us an item's start and end and 8 us the join.  Measured slower: four softmax
+// the softmax left out).  2048 tokens over 30K keys, 32 / 8 heads: 852 to 888 us, 1200 to 1250
+// TFLOP/s; a prompt of 8192: 455 to 470 us; four ragged chunks over 12000 keys in pages of 16: 84
+// us, of which about 4 us an item's start and end and 8 us the join.  Measured slower: four softmax
 // warpgroups, 64-key tiles with two sets of scores, exponentials on a polynomial.
 // TMEM columns: S_0 / P_0 [0, 128), S_1 / P_1 [128, 256), O_0 [256, ..), O_1 [384, ..).
 // Keys behind the last visible one: their scores are replaced, and the issuer clears their V

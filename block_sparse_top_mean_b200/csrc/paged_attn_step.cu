@@ -27,7 +27,7 @@ constexpr int kConsumers = 4;         // warps 0-3; warp 4 produces
 constexpr int kThreads = 32 * (kConsumers + 1);
 // Two CTAs an SM: while one joins an item's warps and starts the next, the other's tiles keep
 // coming (256 sequences of up to 256 keys 50 -> 35 us, 48 of 1 to 16384 52 -> 49, 64 x 8192 325
-// -> 316; one CTA of 192 KB: the same bytes in flight).
+// -> 316, against one CTA of 12 stages, 192 KB; two of 4 stages hold 128 KB).
 constexpr int kCtas = 2;
 template <int D> constexpr int kStages = 4 * 128 / D;        // 64 KB of tiles a CTA
 // What an item costs beside its tiles, in tiles (48 sequences of 1 to 16384 keys, one CTA an SM: 0

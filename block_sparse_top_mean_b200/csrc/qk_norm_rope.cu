@@ -300,7 +300,9 @@ __global__ void __launch_bounds__(1024)
 dw_sum_kernel(const float* __restrict__ part, int nq, int n_cta, int d, float* __restrict__ dwq,
               float* __restrict__ dwk) {
   __shared__ float s[32][33];
-  asm volatile("griddepcontrol.wait;" ::: "memory");      // launched beside the kernel above
+  // (launched programmatically: it is set up beside the kernel above, which lets it start when it
+  // has ended)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const bool keys = (int)blockIdx.x >= d / 32;
   const int col = (blockIdx.x - (keys ? d / 32 : 0)) * 32 + x;

@@ -224,7 +224,8 @@ MSA_API msa_status msa_rope_docwise(const msa_params* p, const int32_t* cu_seqle
  *   wq, wk [d]    weights in the tensors' dtype; NULL = ones.
  *   q_out, k_out  [T, hq, d], [T, hkv, d] packed.  They may be q and k themselves where those
  *                 are packed, and may not overlap them otherwise.
- * eps > 0, base > 1.  Norm and rotation in fp32 (angles in fp64), rounded once.  Any
+ * eps > 0, base > 1.  Norm and rotation in fp32 (angles in fp64), rounded once; the sum of a
+ * head's squares is fp32 too, so a head of elements beyond 1.6e18 comes out as zeros.  Any
  * hq / hkv up to 64; d 64 or 128. */
 MSA_API msa_status msa_qk_norm_rope(const msa_params* p, const int32_t* cu_seqlens,
                                     int64_t n_docs, const void* q, int64_t q_stride,
