@@ -192,6 +192,10 @@ def dist_setup():
         if torch.cuda.is_available():
             torch.cuda.set_device(local)
         dist.init_process_group(backend, timeout=datetime.timedelta(seconds=600))
+        if backend == "gloo":
+            # gloo connects every pair here; a rank with nothing to do that left at once could close
+            # its end while another still waits for the connection
+            dist.barrier()
     elif torch.cuda.is_available():
         torch.cuda.set_device(local)
     return world, rank, local
